@@ -27,7 +27,9 @@
  * allocation), smp_repetition_penalty (an in-place logits processor to run
  * before sampling), smp_gumbel_sample (a sort-free Gumbel-max draw over a
  * kept set, for comparison) and smp_spec_verify (speculative-decoding
- * verification against the kept sets' probabilities); smp_set_kernel
+ * verification against the kept sets' probabilities); smp_token_logprobs,
+ * smp_token_logprobs_grad and smp_head_logprobs (scoring of given tokens, for
+ * training on them or reporting them); smp_set_kernel
  * chooses between the two sampler kernels and smp_set_wait_limit bounds the
  * device-side waits.
  *
@@ -295,6 +297,95 @@ int smp_gumbel_sample(smp_handle h, const void* logits, smp_dtype dtype, int B, 
                       const uint32_t* kept_mask, const float* temperature, const uint64_t* seed,
                       const uint64_t* offset, int32_t* tokens, int32_t* row_status,
                       smp_stream stream);
+
+/* ---- Scoring of given tokens ---------------------------------------------
+ * The three calls below take no handle and allocate nothing; they run on the
+ * CURRENT CUDA device, on `stream`.  They use the RAW distribution (no top-k
+ * or top-p): for row r with legal set A = {j < V : bit j of the bitmask row
+ * set, x_j != -inf}, temperature T and m = max over A of x,
+ *     z_j = (x_j - m) / T,   L = log sum_A exp(z_j),   log p_j = z_j - L.
+ * temperature: DEVICE float [B], each finite and > 0 (there is no greedy path
+ * here), or NULL for 1.  targets: DEVICE int32 [B]: a token id in [0, V), or
+ * -1 for a row without one (a padded position, or the token of a row that
+ * failed to sample).  Row status: SMP_ERR_INVALID_PARAM (bad temperature, a
+ * target outside [-1, V)), SMP_ERR_NONFINITE (NaN or +inf in a legal slot),
+ * SMP_ERR_EMPTY (no legal token). */
+
+/* Log-probabilities of given tokens, with entropy, rank and the n most likely
+ * alternatives ("Sampling system design" post, section on logprobs: an API
+ * that returns logprobs states the distribution they are taken under, raw or
+ * processed; smp_sample_logprob has the processed one).  Outputs, DEVICE:
+ *   logprobs    : float [B]: log p of the target; -inf if it is not legal, 0
+ *                 for a row without one.  Required when targets is given.
+ *   entropy     : float [B], nullable: -sum_A p_j log p_j (natural log).
+ *   rank        : int32 [B], nullable: how many legal tokens come before the
+ *                 target by logit (descending, smallest id first among equal
+ *                 logits): 0 = most likely.  A target that is not legal comes
+ *                 after all legal ones; -1 for a row without one.
+ *   stats       : float [B][2], nullable: {m, L}, which
+ *                 smp_token_logprobs_grad takes (m / T + L is the row's
+ *                 logsumexp).
+ *   row_status  : int32 [B], required.
+ *   top_ids     : int32 [B][n], top_logprobs: float [B][n]: the n most likely
+ *                 legal tokens in the order that defines rank, 0 <= n <= 32
+ *                 (NULL allowed when n == 0).  Slots past the legal set get
+ *                 id -1 and -inf.
+ * A row whose status is not SMP_OK gets NaN, rank -1 and ids -1.
+ * Call status: SMP_ERR_INVALID_PARAM for NULL required pointers, B < 0,
+ * V < 1, ld < V, n < 0 or an unknown dtype; SMP_ERR_CAPACITY for n > 32 or
+ * V > 16,777,216; SMP_ERR_CUDA when the launch fails. */
+int smp_token_logprobs(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
+                       const uint32_t* bitmask, const float* temperature, const int32_t* targets,
+                       float* logprobs, float* entropy, int32_t* rank, float* stats,
+                       int32_t* row_status, int n, int32_t* top_ids, float* top_logprobs,
+                       smp_stream stream);
+
+/* Gradient of smp_token_logprobs' logprobs and entropy with respect to the
+ * logits, for a loss with d loss / d logprobs[r] = grad_logprobs[r] and
+ * d loss / d entropy[r] = grad_entropy[r]:
+ *   grad[r][j] = (grad_logprobs[r] (1{j = target} - p_j)
+ *                 - grad_entropy[r] p_j (log p_j + entropy[r])) / T,
+ * computed in binary32 and rounded once to `dtype`; 0 for tokens that are not
+ * legal.  grad_logprobs counts nothing in a row without a target or with one
+ * that is not legal.  A row whose stats are not finite (a row that failed in
+ * the forward call), or whose temperature or target is invalid, gets zeros.
+ *   logits, bitmask, temperature, targets: as given to the forward call.
+ *   stats         : float [B][2], the forward call's.
+ *   entropy       : float [B], the forward call's; needed with grad_entropy.
+ *   grad_logprobs, grad_entropy: float [B], either may be NULL (zero).
+ *   grad          : [B][grad_ld] of dtype, grad_ld >= V; columns from V on
+ *                   are not written.  May be the logits themselves (same
+ *                   pointer and ld): the gradient then replaces them.
+ * Call status as for smp_token_logprobs.  Work: one read of the logits and
+ * one write of the gradient. */
+int smp_token_logprobs_grad(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
+                            const uint32_t* bitmask, const float* temperature,
+                            const int32_t* targets, const float* stats, const float* entropy,
+                            const float* grad_logprobs, const float* grad_entropy, void* grad,
+                            int64_t grad_ld, smp_stream stream);
+
+/* smp_token_logprobs straight from hidden states, without the [N][V] logits
+ * in memory: x_rj = sum_d hidden[r][d] weight[j][d], products and sums in
+ * binary32 (the logits are not rounded to `dtype`).
+ *   hidden : DEVICE [N][ld_hidden], weight: DEVICE [V][ld_weight], both
+ *            SMP_BF16 or both SMP_F16, D values per row; 16-byte aligned
+ *            addresses, ld >= D and a multiple of 8.
+ *   temperature, targets and the outputs: as above with B = N (no bitmask,
+ *            rank or alternatives).  entropy and stats are nullable.
+ *   workspace: DEVICE, 16-byte aligned, at least smp_head_workspace(N, V)
+ *            bytes, used until the call's work on the stream is done.
+ * Call status: SMP_ERR_INVALID_PARAM for NULL required pointers, N < 0, V or
+ * D < 1, a bad ld or alignment, a workspace that is too small, or fp32;
+ * SMP_ERR_CAPACITY for V > 16,777,216, N > 1,048,576 or D > 1,048,576. */
+int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
+                      int64_t ld_weight, smp_dtype dtype, int N, int V, int D,
+                      const float* temperature, const int32_t* targets, float* logprobs,
+                      float* entropy, float* stats, int32_t* row_status, void* workspace,
+                      int64_t workspace_bytes, smp_stream stream);
+
+/* Bytes of workspace that smp_head_logprobs needs for N rows and V tokens (0
+ * for N or V < 1). */
+int64_t smp_head_workspace(int N, int V);
 
 /* Optional per-row diagnostics for subsequent calls on this handle: when
  * row_info is not NULL, each call writes int32 [B][4] to it (DEVICE memory

@@ -18,7 +18,8 @@ _DTYPES = {torch.float32: SMP_F32, torch.bfloat16: SMP_BF16, torch.float16: SMP_
 EXPORTS = ("smp_create", "smp_destroy", "smp_topk_topp_mask", "smp_sample", "smp_argmax",
            "smp_sample_noalloc", "smp_sample_logprob", "smp_spec_verify",
            "smp_repetition_penalty", "smp_gumbel_sample", "smp_top_logprobs", "smp_set_row_info",
-           "smp_set_kernel", "smp_set_wait_limit", "smp_plan",
+           "smp_set_kernel", "smp_set_wait_limit", "smp_plan", "smp_token_logprobs",
+           "smp_token_logprobs_grad", "smp_head_logprobs", "smp_head_workspace",
            "smp_status_string")
 
 
@@ -69,6 +70,12 @@ def load_library(path=None):
     L.smp_set_wait_limit.argtypes = [P, ctypes.c_longlong]
     L.smp_plan.argtypes = [P, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(I),
                            ctypes.POINTER(I)]
+    I64 = ctypes.c_int64
+    L.smp_token_logprobs.argtypes = [P, I, I, I, I64, P, P, P, P, P, P, P, P, I, P, P, P]
+    L.smp_token_logprobs_grad.argtypes = [P, I, I, I, I64, P, P, P, P, P, P, P, P, I64, P]
+    L.smp_head_logprobs.argtypes = [P, I64, P, I64, I, I, I, I, P, P, P, P, P, P, P, I64, P]
+    L.smp_head_workspace.argtypes = [I, I]
+    L.smp_head_workspace.restype = I64
     L.smp_status_string.restype = ctypes.c_char_p
     L.smp_status_string.argtypes = [I]
     for name in EXPORTS:

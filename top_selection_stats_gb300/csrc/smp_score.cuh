@@ -1,0 +1,163 @@
+// smp_score.cuh -- what the scoring kernels (smp_score.cu, smp_score_grad.cu,
+// smp_head.cu) share: the softmax state of a set of values, its merge, and
+// the results computed from it.
+//
+// A set A of values x with largest m, scaled by s = log2(e) / T, is held as
+//     m,  S = sum 2^d,  U = sum 2^d d,   d = (x - m) s <= 0,
+// in binary32.  From it L = ln 2 log2 S and the entropy, ln 2 (log2 S - U/S),
+// a sum of two terms that are both >= 0, so nothing cancels.  x - m is formed
+// before the scaling: near the top, where the mass is, it is exact, so the
+// results do not lose bits when all logits are far from 0.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/smp.h"
+
+namespace smp {
+
+constexpr float SC_LN2 = 0.6931471805599453f;
+// d is clamped here before it is multiplied by 2^d: 2^d is 0 long before, and
+// 0 times the d of an illegal token (-inf) would be NaN.
+constexpr float SC_DMIN = -1.0e4f;
+constexpr int SC_MAX_V = 1 << 24;
+constexpr int SC_MAX_TOP = 32;
+
+__device__ __forceinline__ float sc_nan() { return __int_as_float(0x7fffffff); }
+
+// A valid temperature is finite and > 0; its scale log2(e) / T is kept finite.
+__device__ __forceinline__ bool sc_temperature_ok(float T) { return T > 0.f && T < INFINITY; }
+__device__ __forceinline__ float sc_scale(float T) {
+  return fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f);
+}
+
+__device__ __forceinline__ float sc_ex2(float d) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+  return y;
+}
+
+struct Soft {
+  float m, S, U;
+};
+
+// One more value (x = -inf: none).
+__device__ __forceinline__ void sc_add(Soft& a, float x, float s) {
+  if (x > a.m) {
+    const float d = a.m == -INFINITY ? SC_DMIN : fmaxf((a.m - x) * s, SC_DMIN);
+    const float c = sc_ex2(d);
+    a.U = (a.U + a.S * d) * c;
+    a.S *= c;
+    a.m = x;
+  }
+  const float d = x == -INFINITY ? SC_DMIN : fmaxf((x - a.m) * s, SC_DMIN);
+  const float e = sc_ex2(d);
+  a.S += e;
+  a.U = fmaf(e, d, a.U);
+}
+
+// The state of the union of two sets.  An empty set has m = -inf, S = U = 0.
+__device__ __forceinline__ Soft sc_merge(const Soft& a, const Soft& b, float s) {
+  Soft r;
+  r.m = fmaxf(a.m, b.m);
+  if (r.m == -INFINITY) {
+    r.S = 0.f;
+    r.U = 0.f;
+    return r;
+  }
+  const float da = fmaxf((a.m - r.m) * s, SC_DMIN), db = fmaxf((b.m - r.m) * s, SC_DMIN);
+  const float ca = sc_ex2(da), cb = sc_ex2(db);
+  r.S = a.S * ca + b.S * cb;
+  r.U = (a.U + a.S * da) * ca + (b.U + b.S * db) * cb;
+  return r;
+}
+
+__device__ __forceinline__ Soft sc_shfl_xor(const Soft& a, int o) {
+  Soft b;
+  b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+  b.S = __shfl_xor_sync(0xffffffffu, a.S, o);
+  b.U = __shfl_xor_sync(0xffffffffu, a.U, o);
+  return b;
+}
+
+// What a complete row's state gives.
+__device__ __forceinline__ float sc_log2_mass(const Soft& a) { return log2f(a.S); }
+__device__ __forceinline__ float sc_entropy(const Soft& a) {
+  return fmaxf(SC_LN2 * (log2f(a.S) - a.U / a.S), 0.f);
+}
+__device__ __forceinline__ float sc_logprob(float x, const Soft& a, float T) {
+  if (x == -INFINITY) return -INFINITY;
+  return fminf(__fdiv_rn(x - a.m, T) - SC_LN2 * log2f(a.S), 0.f);
+}
+
+template <int DT>
+struct ScType;
+template <>
+struct ScType<SMP_F32> {
+  using raw = float;
+  static __device__ __forceinline__ float value(float v) { return v; }
+  static __device__ __forceinline__ float store(float v) { return v; }
+};
+template <>
+struct ScType<SMP_BF16> {
+  using raw = unsigned short;
+  static __device__ __forceinline__ float value(unsigned short v) {
+    return __uint_as_float((uint32_t)v << 16);
+  }
+  static __device__ __forceinline__ unsigned short store(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+};
+template <>
+struct ScType<SMP_F16> {
+  using raw = unsigned short;
+  static __device__ __forceinline__ float value(unsigned short v) {
+    return __half2float(__ushort_as_half(v));
+  }
+  static __device__ __forceinline__ unsigned short store(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+  }
+};
+
+struct ScoreArgs {
+  const void* logits;
+  long long ld;
+  const uint32_t* bitmask;
+  const float* temperature;
+  const int32_t* targets;
+  float *logprobs, *entropy, *stats;
+  int32_t *rank, *status, *top_ids;
+  float* top_lp;
+  int B, V, W, n;
+};
+struct GradArgs {
+  const void* logits;
+  long long ld, gld;
+  const uint32_t* bitmask;
+  const float* temperature;
+  const int32_t* targets;
+  const float *stats, *entropy, *g_lp, *g_ent;
+  void* grad;
+  int B, V, W;
+};
+struct HeadArgs {
+  const void *hidden, *weight;
+  long long ldh, ldw;
+  const float* temperature;
+  const int32_t* targets;
+  float *logprobs, *entropy, *stats;
+  int32_t* status;
+  float4* part;  // workspace
+  int N, V, D;
+};
+
+int score_enqueue(const ScoreArgs& a, int dtype, cudaStream_t st);
+int grad_enqueue(const GradArgs& a, int dtype, cudaStream_t st);
+int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st);
+int64_t head_workspace(int N, int V);
+
+}  // namespace smp

@@ -1,0 +1,176 @@
+"""Scoring of given tokens: log probabilities, entropy, rank and alternatives
+under the raw distribution, their gradient, and the same straight from hidden
+states (the handle-free calls of include/smp.h).  Argument marshalling only.
+
+Every tensor lives on the logits' (the hidden states') CUDA device and is
+contiguous; the calls run on that device's current stream.  ``out`` takes what
+an earlier call of the same shape returned and writes it again, so a serving
+loop allocates nothing.
+"""
+import torch
+
+from .binding import _DTYPES, _check, load_library
+
+
+def _stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _need(t, name, dev, dtype, shape):
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name, dev, dtype, shape):
+    return None if t is None else _need(t, name, dev, dtype, shape)
+
+
+def _matrix(t, name, dtypes):
+    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"unsupported {name} dtype {t.dtype}")
+    return t.shape
+
+
+def _width(V, ld, name):
+    V = ld if V is None else V
+    if not 1 <= V <= ld:
+        raise ValueError(f"{name} must be in [1, {ld}], got {V}")
+    return V
+
+
+def _launch(dev, fn, *args):
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
+
+
+def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=None, out=None,
+                   lib=None):
+    """smp_token_logprobs: per row of logits [B, V] (or [B, ld] with ``V``) the
+    log probability of targets[r] (int32 [B]; -1: none) under
+    softmax(logits / temperature) over the legal tokens, the entropy, the
+    target's rank, and the ``n_top`` (<= 32) most likely tokens.
+
+    temperature: float32 [B] or None (1); bitmask: int32 [B, ceil(V/32)] or
+    None.  Returns logprobs, entropy, rank, stats ([B, 2], for
+    token_logprobs_grad), status and, with n_top, top_ids and top_logprobs
+    [B, n_top]."""
+    L = lib or load_library()
+    B, ld = _matrix(logits, "logits", _DTYPES)
+    V = _width(V, ld, "V")
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    tg = _need(targets, "targets", dev, i32, (B,))
+    tp = _opt(temperature, "temperature", dev, f32, (B,))
+    bm = _opt(bitmask, "bitmask", dev, i32, (B, (V + 31) // 32))
+    if n_top < 0:
+        raise ValueError("n_top must be >= 0")
+    if out is None:
+        out = dict(logprobs=torch.empty(B, dtype=f32, device=dev),
+                   entropy=torch.empty(B, dtype=f32, device=dev),
+                   rank=torch.empty(B, dtype=i32, device=dev),
+                   stats=torch.empty((B, 2), dtype=f32, device=dev),
+                   status=torch.empty(B, dtype=i32, device=dev))
+        if n_top:
+            out["top_ids"] = torch.empty((B, n_top), dtype=i32, device=dev)
+            out["top_logprobs"] = torch.empty((B, n_top), dtype=f32, device=dev)
+    rc = _launch(dev, L.smp_token_logprobs, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, bm,
+                 tp, tg, _need(out["logprobs"], "logprobs", dev, f32, (B,)),
+                 _need(out["entropy"], "entropy", dev, f32, (B,)),
+                 _need(out["rank"], "rank", dev, i32, (B,)),
+                 _need(out["stats"], "stats", dev, f32, (B, 2)),
+                 _need(out["status"], "status", dev, i32, (B,)), n_top,
+                 _need(out["top_ids"], "top_ids", dev, i32, (B, n_top)) if n_top else None,
+                 _need(out["top_logprobs"], "top_logprobs", dev, f32, (B, n_top)) if n_top else None)
+    _check(rc, "smp_token_logprobs")
+    return out
+
+
+def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None,
+                        grad_entropy=None, temperature=None, bitmask=None, V=None, out=None,
+                        lib=None):
+    """smp_token_logprobs_grad: the gradient with respect to logits, in their
+    dtype and shape, for d loss / d logprobs = grad_logprobs and d loss /
+    d entropy = grad_entropy (float32 [B], either None).  stats and entropy are
+    the forward call's.  ``out`` may be logits itself (in place); columns past
+    V are zero in a fresh result and are not written in ``out``."""
+    L = lib or load_library()
+    B, ld = _matrix(logits, "logits", _DTYPES)
+    V = _width(V, ld, "V")
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("entropy is required with grad_entropy")
+    if out is None:
+        out = torch.empty_like(logits)
+        if V < ld:
+            out[:, V:].zero_()
+    rc = _launch(dev, L.smp_token_logprobs_grad, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld,
+                 _opt(bitmask, "bitmask", dev, i32, (B, (V + 31) // 32)),
+                 _opt(temperature, "temperature", dev, f32, (B,)),
+                 _need(targets, "targets", dev, i32, (B,)),
+                 _need(stats, "stats", dev, f32, (B, 2)),
+                 _opt(entropy, "entropy", dev, f32, (B,)),
+                 _opt(grad_logprobs, "grad_logprobs", dev, f32, (B,)),
+                 _opt(grad_entropy, "grad_entropy", dev, f32, (B,)),
+                 _need(out, "out", dev, logits.dtype, (B, ld)), ld)
+    _check(rc, "smp_token_logprobs_grad")
+    return out
+
+
+def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, workspace=None,
+                  lib=None):
+    """smp_head_logprobs: token_logprobs' logprobs, entropy, stats and status
+    for logits = hidden @ weight.T (hidden [N, D], weight [V, D], both bfloat16
+    or both float16, row lengths a multiple of 8; with ``D`` only the first D
+    columns count), without the logits in memory.  workspace: uint8, at least
+    head_workspace(N, V) bytes; allocated per call when None."""
+    L = lib or load_library()
+    N, ldh = _matrix(hidden, "hidden", (torch.bfloat16, torch.float16))
+    V, ldw = _matrix(weight, "weight", (torch.bfloat16, torch.float16))
+    dev = hidden.device
+    if weight.dtype != hidden.dtype or weight.device != dev:
+        raise ValueError("hidden and weight must have one dtype and one device")
+    if D is None and ldh != ldw:
+        raise ValueError("hidden and weight must have rows of one length, or D given")
+    D = _width(D, min(ldh, ldw), "D")
+    if ldh % 8 or ldw % 8:
+        raise ValueError("rows of hidden and weight must be a multiple of 8 values long")
+    f32, i32 = torch.float32, torch.int32
+    tg = _need(targets, "targets", dev, i32, (N,))
+    tp = _opt(temperature, "temperature", dev, f32, (N,))
+    if out is None:
+        out = dict(logprobs=torch.empty(N, dtype=f32, device=dev),
+                   entropy=torch.empty(N, dtype=f32, device=dev),
+                   stats=torch.empty((N, 2), dtype=f32, device=dev),
+                   status=torch.empty(N, dtype=i32, device=dev))
+    nbytes = L.smp_head_workspace(N, V)
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+          or not workspace.is_contiguous() or workspace.numel() < nbytes):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on {dev}")
+    rc = _launch(dev, L.smp_head_logprobs, hidden.data_ptr(), ldh, weight.data_ptr(), ldw,
+                 _DTYPES[hidden.dtype], N, V, D, tp, tg,
+                 _need(out["logprobs"], "logprobs", dev, f32, (N,)),
+                 _need(out["entropy"], "entropy", dev, f32, (N,)),
+                 _need(out["stats"], "stats", dev, f32, (N, 2)),
+                 _need(out["status"], "status", dev, i32, (N,)), workspace.data_ptr(),
+                 workspace.numel())
+    _check(rc, "smp_head_logprobs")
+    return out
+
+
+def head_workspace(N, V, lib=None):
+    """smp_head_workspace: bytes of workspace that head_logprobs needs."""
+    return (lib or load_library()).smp_head_workspace(N, V)
