@@ -1,96 +1,355 @@
 // smp_head.cu -- log probabilities and entropy straight from hidden states and
-// the output head's weights (smp_head_logprobs).  Phase 1: a CTA takes 64 rows
-// and a chunk of the vocabulary, forms 64 x 64 tiles of logits from shared
-// memory and folds them into the rows' softmax states; the state and the
-// target's logit, if the chunk holds it, go to the workspace.  Phase 2 joins
-// the chunks of a row.
+// the output head's weights (smp_head_logprobs): logits that only ever exist
+// as accumulators in tensor memory.
+//
+// head_kernel, one persistent CTA per SM, forms tiles of 128 states x BN tokens
+// with tcgen05.mma (16-bit operands, binary32 accumulators).  One thread feeds
+// a ring of TMA stages (64 values of D each, 128-byte swizzle), one thread
+// issues the products, and two groups of four warps, each with half of the
+// tile's columns, read finished accumulators into registers: a thread owns one
+// state's half row, folds it into a softmax state {m, S, U} and writes that to
+// the workspace with the target's logit.
+//
+// The tensor cores' binary32 accumulation drops low bits instead of rounding:
+// over D = 4096 in one accumulator the logits were off by 5e-6 of their size.
+// So an accumulator sums HSEG stages (512 values of D) and the segments are
+// added, rounded to nearest, in the epilogue's registers.  Accumulators are
+// double buffered (512 columns of tensor memory): the epilogue of a segment
+// or tile runs under the products of the next.
+//
+// Tiles are walked with the states fastest: the SMs share a few weight tiles
+// at any time and every weight comes from HBM once; the hidden states stay in
+// L2.  head_join merges the states of a row in a fixed order: the same bits
+// each call.
+//
+// Every wait on a barrier is bounded.  One that expires makes all roles of the
+// CTA leave; copies and products in flight are waited for, tensor memory is
+// freed, and all rows of the call return SMP_ERR_TIMEOUT.
+#include <cuda.h>
+
 #include "smp_score.cuh"
 
 namespace smp {
 namespace {
 
-constexpr int HM = 64, HN = 64, HK = 32;
-constexpr int HCHUNK = 1024;  // tokens a workspace entry stands for
+constexpr int HBM = 128;               // states per tile
+constexpr int HBK = 64;                // values of D per stage: one 128-byte swizzle atom
+constexpr int HSEG = 8;                // stages that one accumulator sums
+constexpr int HEPI = 8;                // epilogue warps: two groups of four
+constexpr int HTHREADS = (HEPI + 2) * 32;
+constexpr int HFLAGS = 1024;           // workspace: one word per CTA, then the tiles' states
+constexpr long long HWAIT = 4000000000ll;  // SM cycles: about two seconds
 
-int chunks_of(int V) { return (V + HCHUNK - 1) / HCHUNK; }
+template <int BN>
+struct HeadShape {
+  static constexpr int A_BYTES = HBM * HBK * 2;
+  static constexpr int B_BYTES = BN * HBK * 2;
+  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int ACCS = 512 / BN;
+  static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + 1024;  // + alignment
+};
 
-template <int DT>
-__global__ void __launch_bounds__(256) head_kernel(const HeadArgs a) {
-  using TY = ScType<DT>;
-  __shared__ float sa[HK][HM + 1], sb[HK][HN + 1], sx[HM][HN + 1];
-  const int r0 = blockIdx.x * HM, chunk = blockIdx.y, tid = threadIdx.x;
-  const int ty = tid / 16, tx = tid % 16;
-  const unsigned short* hid = static_cast<const unsigned short*>(a.hidden);
-  const unsigned short* wei = static_cast<const unsigned short*>(a.weight);
-  const int v1 = min(a.V, (chunk + 1) * HCHUNK);
-  const int row = r0 + tid;
-  const bool mine = tid < HM && row < a.N;
-  const float T = mine && a.temperature ? a.temperature[row] : 1.f;
-  const float s = sc_scale(sc_temperature_ok(T) ? T : 1.f);
-  const int t = mine && a.targets ? a.targets[row] : -1;
-  Soft st{-INFINITY, 0.f, 0.f};
-  float xt = -INFINITY;
-  bool bad = false;
-  for (int v0 = chunk * HCHUNK; v0 < v1; v0 += HN) {
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.D; k0 += HK) {
-      __syncthreads();
-      for (int i = tid; i < HM * HK; i += 256) {
-        const int k = i % HK, m = i / HK;
-        const bool in = k0 + k < a.D;
-        sa[k][m] = in && r0 + m < a.N ? TY::value(hid[(size_t)(r0 + m) * a.ldh + k0 + k]) : 0.f;
-        sb[k][m] = in && v0 + m < a.V ? TY::value(wei[(size_t)(v0 + m) * a.ldw + k0 + k]) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < HK; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sx[ty * 4 + i][tx * 4 + j] = acc[i][j];
-    __syncthreads();
-    if (mine) {
-      for (int j = 0; j < HN && v0 + j < v1; ++j) {
-        const float x = sx[tid][j];
-        if (!(x < INFINITY)) bad = true;
-        else if (x > -INFINITY) sc_add(st, x, s);
-        if (v0 + j == t) xt = x;
-      }
+// Few states: the weights' stream is the bound, and narrower tiles spread it
+// more evenly over the SMs.
+int tile_tokens(int N) { return N <= HBM ? 128 : 256; }
+int tiles_of(int N, int V) { return (V + tile_tokens(N) - 1) / tile_tokens(N); }
+
+struct HeadBars {
+  uint64_t full[8], empty[8], acc_full[4], acc_empty[4], drain;
+  uint32_t tmem;
+  int fail;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(b)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0u;
+}
+// Waits for the phase; false when it does not come within `HWAIT` cycles or
+// another role has given up.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* fail) {
+  if (bar_try(b, parity)) return true;
+  const long long t0 = clock64();
+  while (!bar_try(b, parity)) {
+    if (*fail) return false;
+    if (clock64() - t0 > HWAIT) {
+      *fail = 1;
+      return false;
     }
   }
-  if (mine) {
-    if (bad) st.m = INFINITY;
-    a.part[(size_t)chunk * a.N + row] = make_float4(st.m, st.S, st.U, xt);
+  return true;
+}
+// The same without a look at the flag: for what is in flight when a role leaves.
+__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!bar_try(b, parity) && clock64() - t0 <= HWAIT) {
   }
 }
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+// Shared-memory operand: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__global__ void __launch_bounds__(128) head_join(const HeadArgs a, int chunks) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= a.N) return;
+// 32 columns of this thread's row (the warp's 32 lanes of tensor memory).
+__device__ __forceinline__ void acc_load(uint32_t addr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+
+template <int BN>
+__global__ void __launch_bounds__(HTHREADS, 1)
+    head_kernel(const HeadArgs a, const __grid_constant__ CUtensorMap map_h,
+                const __grid_constant__ CUtensorMap map_w, const uint32_t idesc, const uint32_t a_bytes) {
+  using SH = HeadShape<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ HeadBars bars;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (a.N + HBM - 1) / HBM, vt = (a.V + BN - 1) / BN;
+  const int kt = (a.D + HBK - 1) / HBK;
+  const long long tiles = (long long)mt * vt;
+  volatile int* fail = &bars.fail;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SH::STAGES; ++i) {
+      bar_init(&bars.full[i], 1);
+      bar_init(&bars.empty[i], 1);
+    }
+    for (int i = 0; i < SH::ACCS; ++i) {
+      bar_init(&bars.acc_full[i], 1);
+      bar_init(&bars.acc_empty[i], HEPI);
+    }
+    bar_init(&bars.drain, 1);
+    bars.fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == HEPI + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&bars.tmem)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+
+  if (warp == HEPI) {  // copies
+    if (lane == 0) {
+      uint32_t i = 0;
+      for (long long tile = blockIdx.x; tile < tiles && !*fail; tile += gridDim.x) {
+        const int m0 = (int)(tile % mt) * HBM, v0 = (int)(tile / mt) * BN;
+        for (int k = 0; k < kt; ++k, ++i) {
+          const uint32_t st = i % SH::STAGES, use = i / SH::STAGES;
+          if (use && !bar_wait(&bars.empty[st], (use - 1) & 1, fail)) break;
+          uint8_t* dst = ring + st * (SH::A_BYTES + SH::B_BYTES);
+          bar_expect(&bars.full[st], a_bytes + SH::B_BYTES);
+          tma_tile(dst, &map_h, k * HBK, m0, &bars.full[st]);
+          tma_tile(dst + SH::A_BYTES, &map_w, k * HBK, v0, &bars.full[st]);
+        }
+      }
+      // the last use of each stage: its products are done, or, when a wait ran
+      // out, its copy has at least landed, before the CTA ends
+      for (uint32_t j = i > SH::STAGES ? i - SH::STAGES : 0; j < i; ++j) {
+        if (*fail || !bar_wait(&bars.empty[j % SH::STAGES], (j / SH::STAGES) & 1, fail))
+          bar_drain(&bars.full[j % SH::STAGES], (j / SH::STAGES) & 1);
+      }
+    }
+  } else if (warp == HEPI + 1) {  // products
+    if (lane == 0) {
+      uint32_t i = 0, sg = 0;
+      for (long long tile = blockIdx.x; tile < tiles && !*fail; tile += gridDim.x) {
+        for (int k0 = 0; k0 < kt && !*fail; k0 += HSEG, ++sg) {
+          const uint32_t b = sg % SH::ACCS, use = sg / SH::ACCS;
+          if (use && !bar_wait(&bars.acc_empty[b], (use - 1) & 1, fail)) break;
+          fence_after();
+          const int k1 = min(kt, k0 + HSEG);
+          for (int k = k0; k < k1; ++k, ++i) {
+            const uint32_t st = i % SH::STAGES;
+            if (!bar_wait(&bars.full[st], (i / SH::STAGES) & 1, fail)) break;
+            fence_after();
+            const uint32_t base = smem_addr(ring + st * (SH::A_BYTES + SH::B_BYTES));
+            const uint64_t da = operand_desc(base), db = operand_desc(base + SH::A_BYTES);
+#pragma unroll
+            for (int q = 0; q < HBK / 16; ++q)  // 16 values of D: 32 bytes further in the atom
+              mma(tmem + b * BN, da + 2 * q, db + 2 * q, idesc, k > k0 || q > 0);
+            mma_commit(&bars.empty[st]);
+          }
+          if (!*fail) mma_commit(&bars.acc_full[b]);
+        }
+      }
+      if (*fail) {
+        mma_commit(&bars.drain);
+        bar_drain(&bars.drain, 0);
+      }
+    }
+  } else {  // epilogue: group warp / 4 has half of the tile's columns
+    constexpr int NC = BN / 2;
+    uint32_t sg = 0;
+    bool gone = false;
+    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      float x[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) x[j] = 0.f;
+      const int c0 = (warp >> 2) * NC;
+      for (int k = 0; k < kt; k += HSEG, ++sg) {
+        const uint32_t b = sg % SH::ACCS;
+        // the warp leaves or stays as one: the loads below are the whole warp's
+        gone = !__all_sync(0xffffffffu, bar_wait(&bars.acc_full[b], (sg / SH::ACCS) & 1, fail));
+        if (gone) break;
+        fence_after();
+        const uint32_t acc = tmem + b * BN + c0 + ((uint32_t)(warp & 3) * 32u << 16);
+#pragma unroll
+        for (int c = 0; c < NC; c += 32) {
+          float v[32];
+          acc_load(acc + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[c + j] += v[j];
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.acc_empty[b]);
+      }
+      if (gone) break;
+      const int vtile = (int)(tile / mt), v0 = vtile * BN + c0;
+      const int row = (int)(tile % mt) * HBM + (warp & 3) * 32 + lane;
+      const bool mine = row < a.N;
+      const float T = mine && a.temperature ? a.temperature[row] : 1.f;
+      const float s = sc_scale(sc_temperature_ok(T) ? T : 1.f);
+      const int t = (mine && a.targets ? a.targets[row] : -1) - v0;  // the target's column, if any
+      if (v0 + NC > a.V) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          if (v0 + j >= a.V) x[j] = -INFINITY;
+      }
+      float xt = -INFINITY;
+      if (__any_sync(0xffffffffu, t >= 0 && t < NC)) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          if (t == j) xt = x[j];
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int j = 4; j < NC; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+      const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float mm = m == -INFINITY ? 0.f : m;
+      float S[4] = {0.f, 0.f, 0.f, 0.f}, U[4] = {0.f, 0.f, 0.f, 0.f};
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const float z = (x[j] - mm) * s;
+        nan |= z != z;
+        const float d = fmaxf(z, SC_DMIN), e = sc_ex2(d);
+        S[j & 3] += e;
+        U[j & 3] = fmaf(e, d, U[j & 3]);
+      }
+      if (mine)
+        a.part[HFLAGS / 4 + ((size_t)row * vt + vtile) * 2 + (warp >> 2)] = make_float4(
+            nan ? INFINITY : m, (S[0] + S[1]) + (S[2] + S[3]), (U[0] + U[1]) + (U[2] + U[3]), xt);
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == HEPI + 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+  if (threadIdx.x == 0) reinterpret_cast<int*>(a.part)[blockIdx.x] = bars.fail;
+}
+
+// One CTA per row: the tiles' states merged, the outputs written.  A row has
+// 2 V / BN states: with one warp a row, the load latency of a single row's 2004
+// states took 23 of 196 us (1 x 128256 x 4096).
+constexpr int HJOIN = 128;
+__global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, int ctas) {
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ float4 sw[HJOIN / 32];
   const float T = a.temperature ? a.temperature[row] : 1.f;
   const int t = a.targets ? a.targets[row] : -1;
   const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
   const float s = sc_scale(valid ? T : 1.f);
   Soft st{-INFINITY, 0.f, 0.f};
   float xt = -INFINITY;
-  bool bad = false;
-  for (int c = lane; c < chunks; c += 32) {
-    const float4 p = a.part[(size_t)c * a.N + row];
-    if (p.x == INFINITY) bad = true;
-    else st = sc_merge(st, Soft{p.x, p.y, p.z}, s);
-    xt = fmaxf(xt, p.w);
+  bool bad = false, late = false;
+  for (int c = tid; c < ctas; c += HJOIN) late |= reinterpret_cast<const int*>(a.part)[c] != 0;
+  const float4* part = a.part + HFLAGS / 4 + (size_t)row * parts;
+  for (int c = tid; c < parts; c += 8 * HJOIN) {
+    float4 p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p[i] = c + i * HJOIN < parts ? part[c + i * HJOIN] : make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (p[i].x == INFINITY) bad = true;
+      else st = sc_merge(st, Soft{p[i].x, p[i].y, p[i].z}, s);
+      xt = fmaxf(xt, p[i].w);
+    }
   }
   for (int o = 16; o > 0; o >>= 1) {
     st = sc_merge(st, sc_shfl_xor(st, o), s);
     xt = fmaxf(xt, __shfl_xor_sync(0xffffffffu, xt, o));
   }
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane) return;
-  const int status = !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
+  if (lane == 0) sw[warp] = make_float4(st.m, st.S, st.U, xt);
+  bad = __syncthreads_or(bad);
+  late = __syncthreads_or(late);
+  if (tid) return;
+  for (int w = 1; w < HJOIN / 32; ++w) {
+    st = sc_merge(st, Soft{sw[w].x, sw[w].y, sw[w].z}, s);
+    xt = fmaxf(xt, sw[w].w);
+  }
+  const int status = late ? SMP_ERR_TIMEOUT : !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
                      : st.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
   const bool ok = status == SMP_OK;
   a.status[row] = status;
@@ -102,17 +361,85 @@ __global__ void __launch_bounds__(128) head_join(const HeadArgs a, int chunks) {
   }
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// Rows of D values; boxes of 64 values x `box` rows.  What lies past D or past
+// the last row reads as zero.
+bool tile_map(CUtensorMap* map, const void* base, int dtype, int rows, int D, long long ld, int box) {
+  const EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t boxes[2] = {HBK, (cuuint32_t)box}, ones[2] = {1, 1};
+  return fn(map, dtype == SMP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* ctas) {
+  using SH = HeadShape<BN>;
+  // 8-row granules: of a state tile that N does not fill, only the rows there are are copied
+  const int rows = a.N < HBM ? (a.N + 7) / 8 * 8 : HBM;
+  CUtensorMap mh, mw;
+  if (!tile_map(&mh, a.hidden, dtype, a.N, a.D, a.ldh, rows) ||
+      !tile_map(&mw, a.weight, dtype, a.V, a.D, a.ldw, BN))
+    return SMP_ERR_CUDA;
+  const uint32_t type = dtype == SMP_BF16 ? 1u : 0u;
+  // binary32 accumulators, both operands of `type` and K-major, N = BN, M = 128
+  const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(BN >> 3) << 17) |
+                         ((uint32_t)(HBM >> 4) << 24);
+  if (cudaFuncSetAttribute(head_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) != cudaSuccess)
+    return SMP_ERR_CUDA;
+  const long long tiles = (long long)((a.N + HBM - 1) / HBM) * ((a.V + BN - 1) / BN);
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  *ctas = grid;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(HTHREADS);
+  cfg.dynamicSmemBytes = SH::SMEM;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, head_kernel<BN>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
+             ? SMP_OK : SMP_ERR_CUDA;
+}
+
 }  // namespace
 
-int64_t head_workspace(int N, int V) { return (int64_t)chunks_of(V) * N * (int64_t)sizeof(float4); }
+int64_t head_workspace(int N, int V) {
+  return HFLAGS * 4 + (int64_t)tiles_of(N, V) * 2 * N * (int64_t)sizeof(float4);
+}
 
 int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st) {
-  const int chunks = chunks_of(a.V);
-  const dim3 grid((a.N + HM - 1) / HM, chunks);
-  if (dtype == SMP_BF16) head_kernel<SMP_BF16><<<grid, 256, 0, st>>>(a);
-  else head_kernel<SMP_F16><<<grid, 256, 0, st>>>(a);
-  head_join<<<(a.N + 3) / 4, 128, 0, st>>>(a, chunks);
-  return cudaGetLastError() == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  int dev = 0, sms = 0, ctas = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SMP_ERR_CUDA;
+  if (sms > HFLAGS) sms = HFLAGS;
+  const int rc = tile_tokens(a.N) == 128 ? launch_head<128>(a, dtype, sms, st, &ctas)
+                                         : launch_head<256>(a, dtype, sms, st, &ctas);
+  if (rc != SMP_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.N);
+  cfg.blockDim = dim3(HJOIN);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, head_join, a, 2 * tiles_of(a.N, a.V), ctas) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
 }
 
 }  // namespace smp
