@@ -427,11 +427,9 @@ int64_t head_workspace(int N, int V) {
 }
 
 int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st) {
-  int dev = 0, sms = 0, ctas = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return SMP_ERR_CUDA;
-  if (sms > HFLAGS) sms = HFLAGS;
+  int ctas = 0;
+  const int sms = sc_sm_count();
+  if (sms < 1 || sms > HFLAGS) return SMP_ERR_CUDA;
   const int rc = tile_tokens(a.N) == 128 ? launch_head<128>(a, dtype, sms, st, &ctas)
                                          : launch_head<256>(a, dtype, sms, st, &ctas);
   if (rc != SMP_OK) return rc;

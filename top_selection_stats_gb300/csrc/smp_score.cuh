@@ -41,6 +41,32 @@ __device__ __forceinline__ float sc_ex2(float d) {
   return y;
 }
 
+// Two binary32 values handled by one instruction.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 struct Soft {
   float m, S, U;
 };
@@ -123,6 +149,38 @@ struct ScType<SMP_F16> {
   }
 };
 
+// The values of a 16-byte vector of logits, and back (round to nearest even).
+template <int DT>
+__device__ __forceinline__ void sc_unpack(const uint4& q, float (&f)[DT == SMP_F32 ? 4 : 8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SMP_F32) {
+      f[i] = __uint_as_float(w[i]);
+    } else if constexpr (DT == SMP_BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      f[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xffffu)));
+      f[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint4 sc_pack(const float (&f)[DT == SMP_F32 ? 4 : 8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SMP_F32)
+      w[i] = __float_as_uint(f[i]);
+    else if constexpr (DT == SMP_BF16)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    else
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 struct ScoreArgs {
   const void* logits;
   long long ld;
@@ -154,6 +212,15 @@ struct HeadArgs {
   float4* part;  // workspace
   int N, V, D;
 };
+
+// SMs of the current device; 0 when it cannot be asked.
+inline int sc_sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
 
 int score_enqueue(const ScoreArgs& a, int dtype, cudaStream_t st);
 int grad_enqueue(const GradArgs& a, int dtype, cudaStream_t st);
