@@ -181,6 +181,14 @@ __device__ __forceinline__ uint4 sc_pack(const float (&f)[DT == SMP_F32 ? 4 : 8]
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The two halves of a cluster-wide barrier (a launch without clusters: its CTA).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 struct ScoreArgs {
   const void* logits;
   long long ld;

@@ -24,13 +24,6 @@ constexpr int GU = 2;       // vectors a thread has in flight
 constexpr int GSTEPS = 4;   // steps a CTA takes, at most
 constexpr int GMAXC = 8;    // in place: CTAs of a row, one cluster
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 struct GradRow {
   float m, s, c0, c1, l2, at;
   int t;
