@@ -19,6 +19,8 @@
 // the order in which candidates arrive.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "smp_score.cuh"
 
 namespace cg = cooperative_groups;
@@ -26,9 +28,8 @@ namespace cg = cooperative_groups;
 namespace smp {
 namespace {
 
-constexpr int ST = 256;       // threads
-constexpr int SW = ST / 32;   // warps
-constexpr int SU = 4;         // vectors a thread has in flight
+constexpr int SULOG = 2;
+constexpr int SU = 1 << SULOG;  // vectors a thread has in flight
 constexpr int SBUCKETS = 16;  // buckets per thread, at most
 constexpr int SCAND = 512;    // candidates ranked at a time
 constexpr int SMAXC = 8;      // CTAs of a row, at most
@@ -74,92 +75,114 @@ struct Word {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
   }
+  // the larger of each value; NaN loses
+  static __device__ __forceinline__ uint32_t max_num(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == SMP_F32) asm("max.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if constexpr (DT == SMP_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // A value to raise all smaller ones to without changing a sum: its weight
+  // is 0, it is finite and so is its d.  NONE where the type has none (and for
+  // binary32, where clamping d costs no more).
+  static __device__ __forceinline__ uint32_t floor_of(float m, float s) {
+    if constexpr (DT == SMP_F32) return NONE;
+    const float want = m - __fdividef(160.f, s);
+    uint32_t h;
+    float f;
+    if constexpr (DT == SMP_BF16) {
+      h = __bfloat16_as_ushort(__float2bfloat16_rd(want));
+      f = __uint_as_float(h << 16);
+    } else {
+      h = __half_as_ushort(__float2half_rd(want));
+      f = __half2float(__ushort_as_half((unsigned short)h));
+    }
+    const float d = (f - m) * s;
+    return f > -INFINITY && d <= -150.f && d > -1e30f ? h * 0x00010001u : NONE;
+  }
   // word i of a vector with the values whose bit is 0 replaced by -inf
   static __device__ __forceinline__ uint32_t keep(uint32_t a, uint32_t bits, int i) {
     if constexpr (DT == SMP_F32) return ((bits >> i) & 1u) ? a : NONE;
-    const uint32_t b = bits >> (2 * i);
-    const uint32_t on = ((b & 1u) ? 0x0000ffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u);
+    // the two bits as the signs of a byte each, spread over 16 bits each
+    const uint32_t hi = bits << (30 - 2 * i);
+    uint32_t on;
+    asm("prmt.b32 %0, %1, %2, 0xbbff;" : "=r"(on) : "r"(hi), "r"(hi << 1));
     return (a & on) | (NONE & ~on);
   }
 };
 
+// A vector of a row that is read once (the buckets read again come out of L2).
+__device__ __forceinline__ uint4 load_vector(const uint4* p) {
+  uint4 q;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
+}
+
 // What a CTA hands to the row's first one.
 struct Part {
   float m, S, U;
-  int ahead, bad;
+  int ahead, bad, kept;
 };
 
+template <int ST>
 struct Scratch {
   uint32_t bucket[SBUCKETS * ST];
   unsigned short queue[SBUCKETS * ST];
   uint64_t cand[SCAND];
-  uint64_t tops[SMAXC][SC_MAX_TOP];  // first CTA: the n best of each
+  uint64_t tops[SMAXC][SC_MAX_TOP];  // first CTA: the n best of each, in order
+  uint64_t best[SC_MAX_TOP];
   Part part[SMAXC];                  // first CTA: the states of all
-  Part warp[SW];
-  uint32_t kth[SW];
+  Part warp[ST / 32];
+  uint32_t kth[ST / 32];
   uint64_t bound;
   int queued, found;
 };
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const int nc, const int seg,
-                                                         const int gshift) {
+template <int DT, int ST, bool TOP, bool MASK>
+__global__ void __launch_bounds__(ST, 4 * 256 / ST) score_kernel(const ScoreArgs a, const int nc, const int seg,
+                                                                     const int gshift) {
+  constexpr int SW = ST / 32;
   using TY = ScType<DT>;
   using raw = typename TY::raw;
   using WD = Word<DT>;
   constexpr int VE = 16 / (int)sizeof(raw);
-  __shared__ __align__(16) Scratch sh;
+  __shared__ __align__(16) Scratch<ST> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (nc > 1) cluster_arrive();  // waited for before the first CTA's shared memory is written
   const int r = blockIdx.x / nc, rank_c = blockIdx.x % nc;
   const raw* row = static_cast<const raw*>(a.logits) + (size_t)r * a.ld;
-  const uint32_t* bm = a.bitmask ? a.bitmask + (size_t)r * a.W : nullptr;
-  const float T = a.temperature ? a.temperature[r] : 1.f;
-  const int t = a.targets ? a.targets[r] : -1;
-  const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
-  const float s = sc_scale(valid ? T : 1.f);
-  auto legal = [&](int j) { return !bm || ((__ldg(bm + (j >> 5)) >> (j & 31)) & 1u); };
-  const float xt = valid && t >= 0 && legal(t) ? TY::value(__ldg(row + t)) : -INFINITY;
-  // counted: values at or above this (nothing without a target or a rank)
-  const float xc = valid && t >= 0 && a.rank ? xt : INFINITY;
-
+  const uint32_t* bm = MASK ? a.bitmask + (size_t)r * a.W : nullptr;
+  auto legal = [&](int j) { return !MASK || ((__ldg(bm + (j >> 5)) >> (j & 31)) & 1u); };
   // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
+  // [f0, f1) lie inside the row; what is left at its ends, fewer than 2 VE
+  // values, goes one to a lane of the first CTA's first warp.
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(raw));
-  const int vectors = (a.V + lead + VE - 1) / VE;
-  const int v0 = min(vectors, rank_c * seg), v1 = min(vectors, v0 + seg);
+  const int f0 = lead ? 1 : 0, f1 = max(f0, (a.V + lead) / VE);
+  const int v0 = min(f1, f0 + rank_c * seg), v1 = min(f1, v0 + seg);
   const uint4* src = reinterpret_cast<const uint4*>(row - lead);
-
-  float m = -INFINITY, tmax = -INFINITY, bmax = -INFINITY;
-  f32x2 S2 = pair(0.f, 0.f), U2 = pair(0.f, 0.f);
-  const f32x2 s2 = pair(s, s);
-  int ahead = 0, batch = 0;
-  bool bad = false;
-  if (TOP) {
-    for (int i = tid; i < SBUCKETS * ST; i += ST) sh.bucket[i] = 0u;
-  }
-  const int vend = valid ? v1 : v0;
-  for (int vb = v0; vb < vend; vb += ST * SU, ++batch) {
-    uint4 x[SU];
+  auto load = [&](uint4 (&x)[SU], int vb) {
     uint32_t bits[SU];
 #pragma unroll
     for (int u = 0; u < SU; ++u) {
-      const int v = vb + u * ST + tid, j0 = v * VE - lead;
+      const int v = vb + u * ST + tid;
       x[u] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
-      bits[u] = 0xffffffffu;
+      if (MASK) bits[u] = 0xffffffffu;
       if (v < v1) {
-        if (j0 >= 0 && j0 + VE <= a.V) {
-          x[u] = __ldg(src + v);
-          if (bm) bits[u] = __funnelshift_r(__ldg(bm + (j0 >> 5)), __ldg(bm + ((j0 + VE - 1) >> 5)), j0 & 31);
-        } else {  // an end of the row
-          float f[VE];
-#pragma unroll
-          for (int i = 0; i < VE; ++i)
-            f[i] = j0 + i >= 0 && j0 + i < a.V && legal(j0 + i) ? TY::value(__ldg(row + j0 + i)) : -INFINITY;
-          x[u] = sc_pack<DT>(f);
+        x[u] = load_vector(src + v);
+        if (MASK) {
+          const int j0 = v * VE - lead;
+          bits[u] = __funnelshift_r(__ldg(bm + (j0 >> 5)), __ldg(bm + ((j0 + VE - 1) >> 5)), j0 & 31);
         }
       }
     }
-    if (bm) {
+    if (MASK) {
+      uint32_t all = 0xffffffffu;
+#pragma unroll
+      for (int u = 0; u < SU; ++u) all &= bits[u];
+      if ((all & ((1u << VE) - 1)) == (1u << VE) - 1) return;  // as in most rows
 #pragma unroll
       for (int u = 0; u < SU; ++u) {
         x[u].x = WD::keep(x[u].x, bits[u], 0);
@@ -168,6 +191,31 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
         x[u].w = WD::keep(x[u].w, bits[u], 3);
       }
     }
+  };
+  // The first batch is on its way before the row's parameters are waited for.
+  uint4 x[SU];
+  load(x, v0);
+  const float T = a.temperature ? a.temperature[r] : 1.f;
+  const int t = a.targets ? a.targets[r] : -1;
+  const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
+  const float s = sc_scale(valid ? T : 1.f);
+  const float xt = valid && t >= 0 && legal(t) ? TY::value(__ldg(row + t)) : -INFINITY;
+  // counted: values at or above this (nothing without a target or a rank)
+  const float xc = valid && t >= 0 && a.rank ? xt : INFINITY;
+  int edge = -1;
+  if (rank_c == 0 && warp == 0) {
+    const int head = lead ? min(a.V, VE - lead) : 0;
+    const int j = lane < head ? lane : max(head, f1 * VE - lead) + lane - head;
+    if (j < a.V && legal(j)) edge = j;
+  }
+
+  float m = -INFINITY, tmax = -INFINITY, bmax = -INFINITY;
+  f32x2 S2 = pair(0.f, 0.f), U2 = pair(0.f, 0.f);
+  const f32x2 s2 = pair(s, s);
+  uint32_t low2 = WD::NONE;  // WD::floor_of(m, s)
+  int ahead = 0, batch = 0;
+  bool bad = false;
+  auto fold = [&](uint4 (&x)[SU], int vb) {
     uint32_t wm = WD::NONE;
 #pragma unroll
     for (int u = 0; u < SU; ++u)
@@ -176,21 +224,52 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
     bad |= !(top < INFINITY);
     if (TOP) {
       bmax = fmaxf(bmax, top);
-      if (((batch + 1) & ((1 << gshift) - 1)) == 0 || vb + ST * SU >= vend) {
+      if (((batch + 1) & ((1 << gshift) - 1)) == 0 || vb + ST * SU >= v1) {
         sh.bucket[(batch >> gshift) * ST + tid] = order32(bmax);
         tmax = fmaxf(tmax, bmax);
         bmax = -INFINITY;
       }
     }
-    if (top > -INFINITY) {
-      if (top > m) {
-        const float d = m == -INFINITY ? SC_DMIN : fmaxf((m - top) * s, SC_DMIN);
-        const float e = sc_ex2(d);
-        U2 = mul2(fma2(S2, pair(d, d), U2), pair(e, e));
-        S2 = mul2(S2, pair(e, e));
-        m = top;
+    if (!(top > -INFINITY)) return;
+    if (top > m) {
+      const float d = m == -INFINITY ? SC_DMIN : fmaxf((m - top) * s, SC_DMIN);
+      const float e = sc_ex2(d);
+      U2 = mul2(fma2(S2, pair(d, d), U2), pair(e, e));
+      S2 = mul2(S2, pair(e, e));
+      m = top;
+      low2 = WD::floor_of(m, s);
+    }
+    if (top >= xc) {
+#pragma unroll
+      for (int u = 0; u < SU; ++u) {
+        const int j0 = (vb + u * ST + tid) * VE - lead;
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) ahead += f[i] > xt || (f[i] == xt && j0 + i < t && xt > -INFINITY);
       }
-      const f32x2 mm = pair(-m, -m);
+    }
+    const f32x2 mm = pair(-m, -m);
+    if (low2 != WD::NONE) {
+#pragma unroll
+      for (int u = 0; u < SU; ++u) {
+        x[u].x = WD::max_num(x[u].x, low2);
+        x[u].y = WD::max_num(x[u].y, low2);
+        x[u].z = WD::max_num(x[u].z, low2);
+        x[u].w = WD::max_num(x[u].w, low2);
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          const f32x2 d = mul2(add2(pair(f[i], f[i + 1]), mm), s2);
+          float d0, d1;
+          unpair(d, d0, d1);
+          const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
+          S2 = add2(S2, e);
+          U2 = fma2(e, d, U2);
+        }
+      }
+    } else {
 #pragma unroll
       for (int u = 0; u < SU; ++u) {
         float f[VE];
@@ -206,18 +285,13 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
           U2 = fma2(e, pair(d0, d1), U2);
         }
       }
-      if (top >= xc) {
-#pragma unroll
-        for (int u = 0; u < SU; ++u) {
-          const int j0 = (vb + u * ST + tid) * VE - lead;
-          float f[VE];
-          sc_unpack<DT>(x[u], f);
-#pragma unroll
-          for (int i = 0; i < VE; ++i)
-            ahead += f[i] > xt || (f[i] == xt && j0 + i < t && xt > -INFINITY);
-        }
-      }
     }
+  };
+  for (int vb = v0; vb < v1;) {
+    fold(x, vb);
+    ++batch;
+    vb += ST * SU;
+    if (vb < v1) load(x, vb);
   }
 
   // the CTA's state
@@ -230,12 +304,16 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
     st.S = a0 + a1;
     st.U = b0 + b1;
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    st = sc_merge(st, sc_shfl_xor(st, o), s);
-    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+  const float xe = edge >= 0 ? TY::value(__ldg(row + edge)) : -INFINITY;
+  if (edge >= 0) {
+    bad |= !(xe < INFINITY);
+    sc_add(st, xe, s);
+    ahead += xe >= xc && (xe > xt || (xe == xt && edge < t && xt > -INFINITY));
   }
+  st = sc_warp_merge(st, s);
+  ahead = __reduce_add_sync(0xffffffffu, ahead);
   bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) sh.warp[warp] = Part{st.m, st.S, st.U, ahead, bad};
+  if (lane == 0) sh.warp[warp] = Part{st.m, st.S, st.U, ahead, bad, 0};
 
   // the bound: warps whose 32 threads all had vectors take part
   const int n = a.n;
@@ -256,16 +334,19 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
   }
   __syncthreads();
   if (nc > 1) cluster_wait();
-  if (tid == 0) {
-    Soft b{sh.warp[0].m, sh.warp[0].S, sh.warp[0].U};
-    int ah = sh.warp[0].ahead, bd = sh.warp[0].bad;
-    for (int w = 1; w < SW; ++w) {
-      b = sc_merge(b, Soft{sh.warp[w].m, sh.warp[w].S, sh.warp[w].U}, s);
-      ah += sh.warp[w].ahead;
-      bd |= sh.warp[w].bad;
+  Part* part = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.part[rank_c], 0) : &sh.part[0];
+  if (warp == 0) {
+    const Part w = lane < SW ? sh.warp[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
+    st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
+    ahead = __reduce_add_sync(0xffffffffu, w.ahead);
+    bad = __any_sync(0xffffffffu, w.bad != 0);
+    if (lane == 0) {
+      part->m = st.m;
+      part->S = st.S;
+      part->U = st.U;
+      part->ahead = ahead;
+      part->bad = bad;
     }
-    Part* to = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.part[rank_c], 0) : &sh.part[0];
-    *to = Part{b.m, b.S, b.U, ah, bd};
   }
 
   if (TOP) {
@@ -273,49 +354,60 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
 #pragma unroll
     for (int w = 1; w < SW; ++w) low = min(low, sh.kth[w]);
     if (low == 0u) low = 1u;  // any legal value
-    const int buckets = min(SBUCKETS, (batch + (1 << gshift) - 1) >> gshift);
+    const int buckets = (batch + (1 << gshift) - 1) >> gshift;
     for (int b = 0; b < buckets; ++b)
       if (sh.bucket[b * ST + tid] >= low) sh.queue[atomicAdd(&sh.queued, 1)] = (unsigned short)(b * ST + tid);
     uint64_t bound = (uint64_t)low << 32;
     __syncthreads();
-    const int per = VE * SU << gshift, total = sh.queued * per;
+    const int lv = SULOG + gshift, total = sh.queued << lv;  // vectors of the queued buckets
+    auto offer = [&](float x, int j) {
+      const uint32_t o = order32(x);
+      const uint64_t k = order_key(o, j);
+      if (o && k >= bound && *reinterpret_cast<volatile int*>(&sh.found) <= SCAND) {
+        const int p = atomicAdd(&sh.found, 1);
+        if (p < SCAND) sh.cand[p] = k;
+      }
+    };
+    int found;
     while (true) {
-      for (int i0 = tid; i0 < total; i0 += ST * 4) {
-        float x[4];
-        int id[4];
+      if (edge >= 0) offer(xe, edge);
+      for (int i0 = tid; i0 < total; i0 += ST * 2) {
+        uint4 x[2];
+        int j0[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           const int i = i0 + q * ST;
-          x[q] = -INFINITY;
-          id[q] = 0;
+          x[q] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
+          j0[q] = 0;
           if (i < total) {
-            const int item = sh.queue[i / per], e = i % per;
-            const int v = v0 + (item % ST) + (((item / ST) * SU << gshift) + e / VE) * ST;
-            const int j = v * VE - lead + e % VE;
-            if (v < v1 && j >= 0 && j < a.V && legal(j)) {
-              x[q] = TY::value(__ldg(row + j));
-              id[q] = j;
+            const int item = sh.queue[i >> lv];
+            const int v = v0 + item % ST + (((item / ST) << lv) + (i & ((1 << lv) - 1))) * ST;
+            if (v < v1) {
+              x[q] = __ldg(src + v);
+              j0[q] = v * VE - lead;
             }
           }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t o = order32(x[q]);
-          const uint64_t k = order_key(o, id[q]);
-          if (o && k >= bound && *reinterpret_cast<volatile int*>(&sh.found) <= SCAND) {
-            const int p = atomicAdd(&sh.found, 1);
-            if (p < SCAND) sh.cand[p] = k;
-          }
+        for (int q = 0; q < 2; ++q) {
+          float f[VE];
+          sc_unpack<DT>(x[q], f);
+          const uint32_t wm = WD::max_num(WD::max_num(x[q].x, x[q].y), WD::max_num(x[q].z, x[q].w));
+          if (order32(WD::top(wm)) < (uint32_t)(bound >> 32)) continue;
+#pragma unroll
+          for (int i = 0; i < VE; ++i)
+            if (order32(f[i]) >= (uint32_t)(bound >> 32) && legal(j0[q] + i)) offer(f[i], j0[q] + i);
         }
       }
       __syncthreads();
-      const int found = sh.found;
+      found = sh.found;
       if (found <= SCAND) break;
       // the n-th best of the list bounds the n-th best of all
-#pragma unroll
+#pragma unroll 1
       for (int c = tid; c < SCAND; c += ST) {
         const uint64_t k = sh.cand[c];
         int above = 0;
+#pragma unroll 16
         for (int i = 0; i < SCAND; ++i) above += sh.cand[i] > k;
         if (above == n - 1) sh.bound = k;
       }
@@ -324,15 +416,15 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
       if (tid == 0) sh.found = 0;
       __syncthreads();
     }
-    const int found = sh.found;
-    uint64_t* tops = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.tops[rank_c][0], 0) : &sh.tops[0][0];
-    if (tid < n && tid >= found) tops[tid] = 0ull;
+    uint64_t* to = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.tops[rank_c][0], 0) : &sh.best[0];
     for (int c = tid; c < found; c += ST) {
       const uint64_t k = sh.cand[c];
       int above = 0;
+#pragma unroll 8
       for (int i = 0; i < found; ++i) above += sh.cand[i] > k;
-      if (above < n) tops[above] = k;
+      if (above < n) to[above] = k;
     }
+    if (tid == 0) part->kept = min(found, n);
   }
 
   if (nc > 1) {  // the first CTA has everything; the others may go
@@ -340,63 +432,63 @@ __global__ void __launch_bounds__(ST, 4) score_kernel(const ScoreArgs a, const i
     cluster_arrive();
     cluster_wait();
     if (rank_c) return;
-  } else {
-    __syncthreads();
-  }
-  Soft b{sh.part[0].m, sh.part[0].S, sh.part[0].U};
-  ahead = sh.part[0].ahead;
-  int any = sh.part[0].bad;
-  for (int c = 1; c < nc; ++c) {
-    b = sc_merge(b, Soft{sh.part[c].m, sh.part[c].S, sh.part[c].U}, s);
-    ahead += sh.part[c].ahead;
-    any |= sh.part[c].bad;
-  }
-  const int status = !valid ? SMP_ERR_INVALID_PARAM : any ? SMP_ERR_NONFINITE
-                     : b.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
-  const bool ok = status == SMP_OK;
-  if (tid == 0) {
-    a.status[r] = status;
-    if (a.logprobs) a.logprobs[r] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, b, T);
-    if (a.entropy) a.entropy[r] = ok ? sc_entropy(b) : sc_nan();
-    if (a.rank) a.rank[r] = ok && t >= 0 ? ahead : -1;
-    if (a.stats) {
-      a.stats[2 * (size_t)r] = ok ? b.m : sc_nan();
-      a.stats[2 * (size_t)r + 1] = ok ? SC_LN2 * sc_log2_mass(b) : sc_nan();
-    }
-  }
-  if (TOP) {
-    int32_t* ids = a.top_ids + (size_t)r * n;
-    float* lps = a.top_lp + (size_t)r * n;
-    auto put = [&](int i, uint64_t k) {
-      ids[i] = ok && k ? key_id(k) : -1;
-      lps[i] = !ok ? sc_nan() : k ? sc_logprob(key_value(k), b, T) : -INFINITY;
-    };
-    if (nc == 1) {
-      if (tid < n) put(tid, sh.tops[0][tid]);
-    } else {
-      for (int c = tid; c < nc * n; c += ST) {
-        const uint64_t k = sh.tops[c / n][c % n];
-        // keys of 0 (a CTA with fewer than n legal values) are all alike: by place
-        int above = 0;
-        for (int p = 0; p < nc; ++p)
-          for (int i = 0; i < n; ++i) {
-            const uint64_t o = sh.tops[p][i];
-            above += o > k || (o == k && p * n + i < c);
-          }
-        if (above < n) put(above, k);
+    if (TOP) {  // a key's place: how many keys of each CTA's ordered list are above it
+      for (int c = tid; c < nc * SC_MAX_TOP; c += ST) {
+        const int own = c / SC_MAX_TOP, i = c % SC_MAX_TOP;
+        if (i >= sh.part[own].kept) continue;
+        const uint64_t k = sh.tops[own][i];
+        int above = i;
+#pragma unroll
+        for (int p = 0; p < SMAXC; ++p) {
+          if (p >= nc || p == own) continue;
+          const int kept = sh.part[p].kept;
+          int lo = 0;
+#pragma unroll
+          for (int step = SC_MAX_TOP; step > 0; step >>= 1)
+            if (lo + step <= kept && sh.tops[p][lo + step - 1] > k) lo += step;
+          above += lo;
+        }
+        if (above < n) sh.best[above] = k;
       }
     }
   }
+  __syncthreads();
+  if (warp) return;
+  const Part w = lane < nc ? sh.part[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
+  st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
+  ahead = __reduce_add_sync(0xffffffffu, w.ahead);
+  bad = __any_sync(0xffffffffu, w.bad != 0);
+  const int kept = TOP ? __reduce_add_sync(0xffffffffu, w.kept) : 0;
+  const int status = !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
+                     : st.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
+  const bool ok = status == SMP_OK;
+  if (lane == 0) {
+    a.status[r] = status;
+    if (a.logprobs) a.logprobs[r] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, st, T);
+    if (a.entropy) a.entropy[r] = ok ? sc_entropy(st) : sc_nan();
+    if (a.rank) a.rank[r] = ok && t >= 0 ? ahead : -1;
+    if (a.stats) {
+      a.stats[2 * (size_t)r] = ok ? st.m : sc_nan();
+      a.stats[2 * (size_t)r + 1] = ok ? SC_LN2 * sc_log2_mass(st) : sc_nan();
+    }
+  }
+  if (TOP && lane < n) {
+    const uint64_t k = lane < kept ? sh.best[lane] : 0ull;
+    a.top_ids[(size_t)r * n + lane] = ok && k ? key_id(k) : -1;
+    a.top_lp[(size_t)r * n + lane] = !ok ? sc_nan() : k ? sc_logprob(key_value(k), st, T) : -INFINITY;
+  }
 }
 
-template <int DT>
+// A row short enough for two batches of 64 threads takes a CTA of 64, so that
+// an SM holds 16 rows.
+template <int DT, int ST>
 int launch_score(const ScoreArgs& a, int sms, cudaStream_t st) {
   constexpr int VE = DT == SMP_F32 ? 4 : 8;
-  const int vectors = (a.V + VE - 1) / VE + 1;  // one more than V fills: rows may start inside one
+  const int vectors = a.V / VE;
   constexpr int step = ST * SU;
   int nc = 1;
   while (nc < SMAXC && (long long)a.B * nc < 4LL * sms && vectors > nc * step) nc *= 2;
-  const int seg = ((vectors + nc - 1) / nc + ST - 1) / ST * ST;
+  const int seg = max(1, ((vectors + nc - 1) / nc + ST - 1) / ST) * ST;
   const int batches = (seg + step - 1) / step;
   int gshift = 0;
   while ((batches >> gshift) + 1 > SBUCKETS) ++gshift;
@@ -412,20 +504,27 @@ int launch_score(const ScoreArgs& a, int sms, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = nc > 1 ? 1 : 0;
-  const cudaError_t e = a.n ? cudaLaunchKernelEx(&cfg, score_kernel<DT, true>, a, nc, seg, gshift)
-                            : cudaLaunchKernelEx(&cfg, score_kernel<DT, false>, a, nc, seg, gshift);
+  const auto kernel = a.n ? (a.bitmask ? score_kernel<DT, ST, true, true> : score_kernel<DT, ST, true, false>)
+                          : (a.bitmask ? score_kernel<DT, ST, false, true> : score_kernel<DT, ST, false, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift);
   return e == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+}
+
+template <int DT>
+int choose_score(const ScoreArgs& a, cudaStream_t st) {
+  const int sms = sc_sm_count();
+  if (sms < 1) return SMP_ERR_CUDA;
+  return a.V <= 2 * 64 * SU * (DT == SMP_F32 ? 4 : 8) ? launch_score<DT, 64>(a, sms, st)
+                                                     : launch_score<DT, 256>(a, sms, st);
 }
 
 }  // namespace
 
 int score_enqueue(const ScoreArgs& a, int dtype, cudaStream_t st) {
-  const int sms = sc_sm_count();
-  if (sms < 1) return SMP_ERR_CUDA;
   switch (dtype) {
-    case SMP_F32: return launch_score<SMP_F32>(a, sms, st);
-    case SMP_BF16: return launch_score<SMP_BF16>(a, sms, st);
-    default: return launch_score<SMP_F16>(a, sms, st);
+    case SMP_F32: return choose_score<SMP_F32>(a, st);
+    case SMP_BF16: return choose_score<SMP_BF16>(a, st);
+    default: return choose_score<SMP_F16>(a, st);
   }
 }
 

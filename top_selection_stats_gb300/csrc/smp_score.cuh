@@ -110,6 +110,24 @@ __device__ __forceinline__ Soft sc_shfl_xor(const Soft& a, int o) {
   return b;
 }
 
+// The warp's union, in every lane: one rescaling to the common largest, then sums.
+__device__ __forceinline__ Soft sc_warp_merge(Soft a, float s) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float d = a.m == -INFINITY ? SC_DMIN : fmaxf((a.m - m) * s, SC_DMIN);
+  const float c = sc_ex2(d);
+  a.U = (a.U + a.S * d) * c;
+  a.S *= c;
+  a.m = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.S += __shfl_xor_sync(0xffffffffu, a.S, o);
+    a.U += __shfl_xor_sync(0xffffffffu, a.U, o);
+  }
+  return a;
+}
+
 // What a complete row's state gives.
 __device__ __forceinline__ float sc_log2_mass(const Soft& a) { return log2f(a.S); }
 __device__ __forceinline__ float sc_entropy(const Soft& a) {
