@@ -248,7 +248,9 @@ inline int sc_sm_count() {
   return sms;
 }
 
-int score_enqueue(const ScoreArgs& a, int dtype, cudaStream_t st);
+int score_f32(const ScoreArgs& a, cudaStream_t st);
+int score_bf16(const ScoreArgs& a, cudaStream_t st);
+int score_f16(const ScoreArgs& a, cudaStream_t st);
 int grad_enqueue(const GradArgs& a, int dtype, cudaStream_t st);
 int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st);
 int64_t head_workspace(int N, int V);

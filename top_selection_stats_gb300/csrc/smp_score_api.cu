@@ -41,7 +41,8 @@ int smp_token_logprobs(const void* logits, smp_dtype dtype, int B, int V, int64_
   a.V = V;
   a.W = (V + 31) / 32;
   a.n = n;
-  return score_enqueue(a, (int)dtype, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  return dtype == SMP_F32 ? score_f32(a, st) : dtype == SMP_BF16 ? score_bf16(a, st) : score_f16(a, st);
 }
 
 int smp_token_logprobs_grad(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,

@@ -1,0 +1,657 @@
+// smp_score_kernel.cuh -- log probabilities of given tokens, entropy, rank and
+// the n most likely alternatives (smp_token_logprobs), in one pass over each
+// row; instantiated per type in smp_score_{f32,bf16,f16}.cu.
+//
+// A row is cut into segments, one per CTA of a cluster of 1 to 8.  A warp takes
+// chunks of 32 x NU 16-byte vectors and folds each, after one look at every
+// lane's maximum, into the lanes' softmax states (smp_score.cuh); the target's
+// rank is counted only by lanes that hold something at or above its logit.
+//   Short segments (one chunk a warp): every load is issued at once, before the
+//   row's parameters arrive, and the chunk stays in registers.
+//   Long segments: each warp streams its chunks through a ring of its own in
+//   shared memory (bulk copies, one mbarrier a stage), so that the bytes in
+//   flight do not depend on registers and no warp waits for another.
+//
+// Alternatives: the warps' q largest lane maxima, 64 values over the cluster, are
+// distinct elements of the row, so the n-th largest of them bounds the n-th
+// best from below; hardly more than n values lie above it.  They are taken from
+// the registers (short) or from the few buckets, groups of one lane's chunks,
+// whose maximum reaches the bound, read again (long), and ranked by counting
+// in a list of SCAND.  When more are found (ties, rows sorted by id), the n-th
+// best of those in the list is a better bound, and the search is repeated with
+// it until the list holds them all.  Keys are (logit, smallest id first), all
+// different, so the result is exact and the same whatever the order in which
+// candidates arrive.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "smp_device.cuh"
+#include "smp_score.cuh"
+
+#ifndef SSTAGES_
+#define SSTAGES_ 2
+#define SLOCC_ 3
+#define SROWS_ 3
+#define SLNU_ 3
+#endif
+namespace smp {
+namespace {
+
+constexpr int SBUCKETS = 8;   // buckets per thread, at most (long segments)
+constexpr int SCAND = 512;    // candidates ranked at a time
+constexpr int SMAXC = 8;      // CTAs of a row, at most
+constexpr int SKEPT = 64;      // short segments: vectors with candidates kept in shared memory
+constexpr int SFIRST = 64;    // values the first bound is taken from
+constexpr int SLNU = SLNU_;
+constexpr int SSTAGES = SSTAGES_;    // ring: chunks in flight per warp
+constexpr float SLAG = 8.f;
+constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
+
+// Order key of a value: larger = earlier; 0 = none (not legal).
+__device__ __forceinline__ uint32_t order32(float x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 folds onto +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(uint32_t o, int id) {
+  return ((uint64_t)o << 32) | (uint64_t)(0xffffffffu - (uint32_t)id);
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t b = (uint32_t)(k >> 32);
+  return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
+}
+__device__ __forceinline__ int key_id(uint64_t k) { return (int)(0xffffffffu - (uint32_t)k); }
+
+// A word of a vector: one binary32 value or two 16-bit ones.
+template <int DT>
+struct Word {
+  static constexpr uint32_t NONE = DT == SMP_F32 ? 0xff800000u : DT == SMP_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+  // maximum of each value; NaN wins
+  static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == SMP_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if constexpr (DT == SMP_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // the larger value; NaN wins
+  static __device__ __forceinline__ float top(uint32_t a) {
+    if constexpr (DT == SMP_F32) return __uint_as_float(a);
+    float x, y, r;
+    if constexpr (DT == SMP_BF16) {
+      x = __uint_as_float(a << 16);
+      y = __uint_as_float(a & 0xffff0000u);
+    } else {
+      x = __half2float(__ushort_as_half((unsigned short)(a & 0xffffu)));
+      y = __half2float(__ushort_as_half((unsigned short)(a >> 16)));
+    }
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+  }
+  // the larger of each value; NaN loses
+  static __device__ __forceinline__ uint32_t max_num(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == SMP_F32) asm("max.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if constexpr (DT == SMP_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // A value to raise all smaller ones to without changing a sum: its weight
+  // is 0, it is finite and so is its d.  NONE where the type has none (and for
+  // binary32, where clamping d costs no more).
+  static __device__ __forceinline__ uint32_t floor_of(float m, float s) {
+    if constexpr (DT == SMP_F32) return NONE;
+    const float want = m - __fdividef(160.f, s);
+    uint32_t h;
+    float f;
+    if constexpr (DT == SMP_BF16) {
+      h = __bfloat16_as_ushort(__float2bfloat16_rd(want));
+      f = __uint_as_float(h << 16);
+    } else {
+      h = __half_as_ushort(__float2half_rd(want));
+      f = __half2float(__ushort_as_half((unsigned short)h));
+    }
+    const float d = (f - m) * s;
+    return f > -INFINITY && d <= -150.f && d > -1e30f ? h * 0x00010001u : NONE;
+  }
+  // word i of a vector with the values whose bit is 0 replaced by -inf
+  static __device__ __forceinline__ uint32_t keep(uint32_t a, uint32_t bits, int i) {
+    if constexpr (DT == SMP_F32) return ((bits >> i) & 1u) ? a : NONE;
+    // the two bits as the signs of a byte each, spread over 16 bits each
+    const uint32_t hi = bits << (30 - 2 * i);
+    uint32_t on;
+    asm("prmt.b32 %0, %1, %2, 0xbbff;" : "=r"(on) : "r"(hi), "r"(hi << 1));
+    return (a & on) | (NONE & ~on);
+  }
+};
+
+// A vector of a row that is read once.
+__device__ __forceinline__ uint4 load_vector(const uint4* p) {
+  uint4 q;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
+}
+
+// The mask's bits for a chunk whose first element is j0 (>= 0), as words that start
+// there; word i is lane i % 32's [i / 32].  Elements past W words read as 0.
+template <int NW>
+__device__ __forceinline__ void load_bits(uint32_t (&w)[NW], const uint32_t* bm, int W, int j0, int words) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    const int k = (j0 >> 5) + i * 32 + lane;
+    const bool in = i * 32 + lane < words;
+    const uint32_t lo = in && k < W ? __ldg(bm + k) : 0u;
+    const uint32_t hi = in && (j0 & 31) && k + 1 < W ? __ldg(bm + k + 1) : 0u;
+    w[i] = __funnelshift_r(lo, hi, j0 & 31);
+  }
+}
+
+enum { SC_NONFINITE = 1, SC_LATE = 2 };
+
+// What a CTA hands to the row's first one.
+struct Part {
+  float m, S, U;
+  int ahead, bad, kept;
+};
+
+// What the search for alternatives uses; long segments put it where the ring was.
+template <int ST, bool LONG>
+struct Lists {
+  uint64_t cand[SCAND];
+  uint64_t tops[SMAXC][SC_MAX_TOP];  // first CTA: the n best of each
+  uint64_t all[SMAXC * SC_MAX_TOP];
+  uint64_t best[SC_MAX_TOP];
+  uint32_t first[SFIRST];
+  // long: buckets to read again; short: vectors, the first SKEPT of them kept
+  unsigned short queue[(LONG ? SBUCKETS : 8) * ST];
+  uint4 kept[LONG ? 1 : SKEPT];
+};
+
+template <int ST, bool LONG, bool TOP>
+struct Scratch {
+  static constexpr int SW = ST / 32;
+  alignas(16) unsigned char lists[TOP && !LONG ? sizeof(Lists<ST, LONG>) : 16];
+  uint64_t full[LONG ? SW * SSTAGES : 1];
+  uint32_t bucket[LONG && TOP ? SBUCKETS * ST : 1];
+  Part part[SMAXC];  // first CTA: the states of all
+  Part warp[SW];
+  uint32_t kth[SFIRST];
+  uint64_t bound;
+  uint32_t low;
+  int queued, found;
+};
+
+template <int DT, int ST, bool LONG, bool TOP, bool MASK>
+__global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
+    score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift) {
+  const int nc = ST == 256 ? row_ctas : 1;  // CTAs of 64 threads have whole rows
+  using TY = ScType<DT>;
+  using raw = typename TY::raw;
+  using WD = Word<DT>;
+  constexpr int SW = ST / 32;
+  constexpr int VE = 16 / (int)sizeof(raw);
+  constexpr int NU = LONG ? 1 << SLNU : 8;  // vectors of a lane in a chunk
+  constexpr int CV = 32 * NU;               // vectors of a chunk
+  constexpr int NW = (CV * VE / 32 + 31) / 32;  // mask words of a lane
+  __shared__ __align__(16) Scratch<ST, LONG, TOP> sh;
+  extern __shared__ __align__(128) uint8_t ring_raw[];
+  using LI = Lists<ST, LONG>;
+  static_assert(!LONG || sizeof(LI) <= (ST * 16 << SLNU) * SSTAGES, "the lists fit where the ring was");
+  LI& li = *reinterpret_cast<LI*>(LONG ? ring_raw : sh.lists);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = blockIdx.x / nc, rank_c = blockIdx.x % nc;
+  const raw* row = static_cast<const raw*>(a.logits) + (size_t)r * a.ld;
+  const uint32_t* bm = MASK ? a.bitmask + (size_t)r * a.W : nullptr;
+  auto legal = [&](int j) { return !MASK || ((__ldg(bm + (j >> 5)) >> (j & 31)) & 1u); };
+
+  // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
+  // [f0, f1) lie inside the row; what is left at its ends, fewer than 2 VE
+  // values, goes one to a lane of the first CTA's first warp.
+  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(raw));
+  const int f0 = lead ? 1 : 0, f1 = max(f0, (a.V + lead) / VE);
+  const int v0 = min(f1, f0 + rank_c * seg), v1 = min(f1, v0 + seg);
+  const uint4* src = reinterpret_cast<const uint4*>(row - lead);
+  const int mine = v0 + warp * CV;  // this warp's first chunk; the next SW * CV further
+
+  uint4 x[NU];
+  uint32_t bits[MASK ? NW : 1];
+  uint4* ring = reinterpret_cast<uint4*>(ring_raw) + warp * (SSTAGES * CV);
+  uint64_t* full = sh.full + (LONG ? warp * SSTAGES : 0);
+  auto fetch = [&](int i) {  // chunk i into its stage; what it does not fill holds nothing
+    const int c = mine + i * (SW * CV), k = min(CV, v1 - c);
+    if (k <= 0) return;
+    uint4* stage = ring + (i % SSTAGES) * CV;
+    for (int e = k + lane; e < CV; e += 32) stage[e] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[i % SSTAGES], k * 16);
+      bulk_g2s(stage, src + c, k * 16, &full[i % SSTAGES]);
+    }
+  };
+  if (LONG) {
+    if (lane == 0) {
+      for (int i = 0; i < SSTAGES; ++i) mbar_init(&full[i], 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    for (int i = 0; i < SSTAGES; ++i) fetch(i);
+    __syncwarp();
+  } else {  // on its way before the row's parameters are waited for
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int v = mine + u * 32 + lane;
+      x[u] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
+      if (v < v1) x[u] = load_vector(src + v);
+    }
+  }
+  if (MASK && mine < v1) load_bits(bits, bm, a.W, mine * VE - lead, CV * VE / 32);
+
+  const float T = a.temperature ? a.temperature[r] : 1.f;
+  const int t = a.targets ? a.targets[r] : -1;
+  const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
+  const float s = sc_scale(valid ? T : 1.f);
+  const float xt = valid && t >= 0 && legal(t) ? TY::value(__ldg(row + t)) : -INFINITY;
+  // counted: values at or above this (nothing without a target or a rank)
+  const float xc = valid && t >= 0 && a.rank ? xt : INFINITY;
+  int edge = -1;
+  if (rank_c == 0 && warp == 0) {
+    const int head = lead ? min(a.V, VE - lead) : 0;
+    const int j = lane < head ? lane : max(head, f1 * VE - lead) + lane - head;
+    if (j < a.V && legal(j)) edge = j;
+  }
+
+  // The lane's sums are relative to ref, which follows its largest value mx only
+  // when that has left it by a factor of 2^SLAG: most chunks have a lane with
+  // a new largest value, few one that is far above.
+  float ref = -INFINITY, mx = -INFINITY;
+  f32x2 S2 = pair(0.f, 0.f), U2 = pair(0.f, 0.f);
+  const f32x2 s2 = pair(s, s);
+  uint32_t low2 = WD::NONE;  // WD::floor_of(ref, s)
+  int ahead = 0, bad = 0;
+  // x: the chunk whose first vector is c
+  auto mask_chunk = [&]() {
+    bool whole = true;
+    uint32_t b[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int word = u * (32 * VE / 32) + lane * VE / 32;  // VE bits of it
+      b[u] = __shfl_sync(0xffffffffu, bits[(u * VE) / 32], word & 31) >> (lane * VE & 31);
+      whole = whole && (b[u] & ((1u << VE) - 1)) == (1u << VE) - 1;
+    }
+    if (whole) return;  // as in most rows
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      x[u].x = WD::keep(x[u].x, b[u], 0);
+      x[u].y = WD::keep(x[u].y, b[u], 1);
+      x[u].z = WD::keep(x[u].z, b[u], 2);
+      x[u].w = WD::keep(x[u].w, b[u], 3);
+    }
+  };
+  auto chunk_top = [&]() {
+    uint32_t wm = WD::NONE;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      wm = WD::max_nan(wm, WD::max_nan(WD::max_nan(x[u].x, x[u].y), WD::max_nan(x[u].z, x[u].w)));
+    return WD::top(wm);
+  };
+  auto fold = [&](int c, float top) {
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(top));
+    const bool raise = (top - ref) * s > SLAG;
+    if (__any_sync(0xffffffffu, raise)) {
+      const float d = !raise ? 0.f : ref == -INFINITY ? SC_DMIN : fmaxf((ref - top) * s, SC_DMIN);
+      const float e = sc_ex2(d);
+      U2 = mul2(fma2(S2, pair(d, d), U2), pair(e, e));
+      S2 = mul2(S2, pair(e, e));
+      if (raise) ref = top;
+      low2 = WD::floor_of(ref, s);
+    }
+    if (__any_sync(0xffffffffu, top >= xc)) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int j0 = (c + u * 32 + lane) * VE - lead;
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) ahead += f[i] > xt || (f[i] == xt && j0 + i < t && xt > -INFINITY);
+      }
+    }
+    const float base = ref == -INFINITY ? 0.f : -ref;
+    const f32x2 mm = pair(base, base);
+    if (__all_sync(0xffffffffu, low2 != WD::NONE)) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        float f[VE];
+        sc_unpack<DT>(make_uint4(WD::max_num(x[u].x, low2), WD::max_num(x[u].y, low2),
+                                 WD::max_num(x[u].z, low2), WD::max_num(x[u].w, low2)), f);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          const f32x2 d = mul2(add2(pair(f[i], f[i + 1]), mm), s2);
+          float d0, d1;
+          unpair(d, d0, d1);
+          const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
+          S2 = add2(S2, e);
+          U2 = fma2(e, d, U2);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          float d0, d1;
+          unpair(mul2(add2(pair(f[i], f[i + 1]), mm), s2), d0, d1);
+          d0 = fmaxf(d0, SC_DMIN);
+          d1 = fmaxf(d1, SC_DMIN);
+          const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
+          S2 = add2(S2, e);
+          U2 = fma2(e, pair(d0, d1), U2);
+        }
+      }
+    }
+  };
+
+  const int chunks = max(0, (v1 - mine + SW * CV - 1) / (SW * CV));  // of this warp
+  if (LONG) {
+    float bmax = -INFINITY;
+    for (int i = 0; i < chunks; ++i) {
+      const int c = mine + i * (SW * CV), st = i % SSTAGES;
+      uint32_t next[MASK ? NW : 1];
+      if (MASK && i + 1 < chunks) load_bits(next, bm, a.W, (c + SW * CV) * VE - lead, CV * VE / 32);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (i / SSTAGES) & 1, SWAIT))) {
+        // the copies behind it are given as long, then the CTA goes on without
+        for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
+          mbar_wait_bounded(&full[k % SSTAGES], (k / SSTAGES) & 1, SWAIT);
+        bad = SC_LATE;
+        break;
+      }
+#pragma unroll
+      for (int u = 0; u < NU; ++u) x[u] = ring[st * CV + u * 32 + lane];
+      __syncwarp();
+      fetch(i + SSTAGES);
+      if (MASK) {
+        mask_chunk();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) bits[w] = next[w];
+      }
+      const float top = chunk_top();
+      fold(c, top);
+      if constexpr (TOP) {
+        bmax = fmaxf(bmax, top);
+        if (((i + 1) & ((1 << gshift) - 1)) == 0 || i + 1 == chunks) {
+          sh.bucket[(i >> gshift) * ST + tid] = order32(bmax);
+          bmax = -INFINITY;
+        }
+      }
+    }
+  } else if (chunks) {
+    if (MASK) mask_chunk();
+    fold(mine, chunk_top());
+  }
+
+  // the CTA's state
+  Soft st;
+  {
+    float a0, a1, b0, b1;
+    unpair(S2, a0, a1);
+    unpair(U2, b0, b1);
+    const float d = mx == -INFINITY ? 0.f : (ref - mx) * s, c = sc_ex2(d);  // from ref to mx
+    st.m = mx;
+    st.S = (a0 + a1) * c;
+    st.U = (b0 + b1 + (a0 + a1) * d) * c;
+    if (!(mx < INFINITY)) bad |= SC_NONFINITE;
+  }
+  const float xe = edge >= 0 ? TY::value(__ldg(row + edge)) : -INFINITY;
+  if (edge >= 0) {
+    if (!(xe < INFINITY)) bad |= SC_NONFINITE;
+    sc_add(st, xe, s);
+    ahead += xe >= xc && (xe > xt || (xe == xt && edge < t && xt > -INFINITY));
+  }
+  st = sc_warp_merge(st, s);
+  ahead = __reduce_add_sync(0xffffffffu, ahead);
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 0) sh.warp[warp] = Part{st.m, st.S, st.U, ahead, bad, 0};
+
+  const int n = a.n;
+  const int q = TOP ? min(SFIRST / (nc * SW), n) : 0;
+  if constexpr (TOP) {  // the warp's q largest lane maxima
+    uint32_t key = order32(mx), mineq = 0u;
+    for (int k = 0; k < q; ++k) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+      const uint32_t who = __ballot_sync(0xffffffffu, key == top);
+      if (lane == __ffs(who) - 1) key = 0u;
+      if (lane == k) mineq = top;
+    }
+    if (lane < q) sh.kth[warp * q + lane] = mineq;
+    if (tid == 0) sh.queued = sh.found = 0;
+  }
+  if (nc > 1) {  // all CTAs of the row have started, and have their maxima in place
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  Part* part = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.part[rank_c], 0) : &sh.part[0];
+  if (nc > 1 && warp == SW - 1) {
+    const Part w = lane < SW ? sh.warp[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
+    st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
+    ahead = __reduce_add_sync(0xffffffffu, w.ahead);
+    bad = __reduce_or_sync(0xffffffffu, w.bad);
+    if (lane == 0) {
+      part->m = st.m;
+      part->S = st.S;
+      part->U = st.U;
+      part->ahead = ahead;
+      part->bad = bad;
+    }
+  }
+
+  if constexpr (TOP) {
+    if (tid < SFIRST) {
+      const int each = SW * q, owner = tid / each;
+      uint32_t v = 0u;
+      if (owner < nc) v = nc > 1 ? *cg::this_cluster().map_shared_rank(&sh.kth[tid % each], owner) : sh.kth[tid];
+      li.first[tid] = v;
+    }
+    __syncthreads();
+    if (tid < SFIRST) {
+      const uint32_t v = li.first[tid];
+      int above = 0;
+#pragma unroll 16
+      for (int i = 0; i < SFIRST; ++i) above += li.first[i] > v || (li.first[i] == v && i < tid);
+      if (above == n - 1) sh.low = max(v, 1u);  // 0: fewer than n; any legal value
+    }
+    __syncthreads();
+    const uint32_t low = sh.low;
+    uint64_t bound = (uint64_t)low << 32;
+    auto offer = [&](float y, int j) {
+      const uint32_t o = order32(y);
+      const uint64_t k = order_key(o, j);
+      if (o && k >= bound && *reinterpret_cast<volatile int*>(&sh.found) <= SCAND) {
+        const int p = atomicAdd(&sh.found, 1);
+        if (p < SCAND) li.cand[p] = k;
+      }
+    };
+    // the vector's values at or above the bound
+    auto offer_vector = [&](const uint4& y, int j0, bool masked) {
+      float f[VE];
+      sc_unpack<DT>(y, f);
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+        if (order32(f[i]) >= (uint32_t)(bound >> 32) && (!masked || legal(j0 + i))) offer(f[i], j0 + i);
+    };
+    if constexpr (LONG) {
+      const int buckets = (chunks + (1 << gshift) - 1) >> gshift;
+      for (int b = 0; b < buckets; ++b)
+        if (sh.bucket[b * ST + tid] >= low) li.queue[atomicAdd(&sh.queued, 1)] = (unsigned short)(b * ST + tid);
+    } else if (order32(mx) >= low) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const uint32_t wm = WD::max_num(WD::max_num(x[u].x, x[u].y), WD::max_num(x[u].z, x[u].w));
+        if (order32(WD::top(wm)) >= low) {
+          const int p = atomicAdd(&sh.queued, 1);
+          li.queue[p] = (unsigned short)(warp * CV + u * 32 + lane);
+          if (p < SKEPT) li.kept[p] = x[u];
+        }
+      }
+    }
+    __syncthreads();
+    const int lv = LONG ? SLNU + gshift : 0, total = sh.queued << lv;  // vectors to look through
+    int found;
+    while (true) {
+      if (edge >= 0) offer(xe, edge);
+#pragma unroll 1
+      for (int i0 = tid; i0 < total; i0 += ST * 2) {
+        uint4 y[2];
+        int j0[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = i0 + h * ST;
+          y[h] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
+          j0[h] = 0;
+          if (i >= total) continue;
+          const int item = li.queue[i >> lv];
+          int v = v0 + item;
+          if constexpr (LONG) {
+            const int e = i & ((1 << lv) - 1), th = item % ST;
+            v = v0 + ((((item / ST) << gshift) + (e >> SLNU)) * SW + th / 32) * CV + (e % NU) * 32 + th % 32;
+          }
+          if (v < v1) {
+            y[h] = !LONG && i < SKEPT ? li.kept[i] : __ldg(src + v);
+            j0[h] = v * VE - lead;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) offer_vector(y[h], j0[h], LONG || i0 + h * ST >= SKEPT);
+      }
+      __syncthreads();
+      found = sh.found;
+      if (found <= SCAND) break;
+      // the n-th best of the list bounds the n-th best of all
+#pragma unroll 1
+      for (int c = tid; c < SCAND; c += ST) {
+        const uint64_t k = li.cand[c];
+        int above = 0;
+#pragma unroll 16
+        for (int i = 0; i < SCAND; ++i) above += li.cand[i] > k;
+        if (above == n - 1) sh.bound = k;
+      }
+      __syncthreads();
+      bound = sh.bound;
+      if (tid == 0) sh.found = 0;
+      __syncthreads();
+    }
+    uint64_t* to = nc > 1 ? cg::this_cluster().map_shared_rank(&li.tops[rank_c][0], 0) : &li.best[0];
+    for (int c = tid; c < found; c += ST) {
+      const uint64_t k = li.cand[c];
+      int above = 0;
+#pragma unroll 8
+      for (int i = 0; i < found; ++i) above += li.cand[i] > k;
+      if (above < n) to[above] = k;
+    }
+    if (tid == 0) part->kept = min(found, n);
+  }
+
+  if (nc > 1) {  // the first CTA has everything; the others may go
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank_c) return;
+    if constexpr (TOP) {  // the CTAs' lists in one, then each key's place in it
+      const int p = tid / SC_MAX_TOP, i = tid % SC_MAX_TOP;
+      int at = 0, total = 0;
+      for (int o = 0; o < nc; ++o) {
+        if (o < p) at += sh.part[o].kept;
+        total += sh.part[o].kept;
+      }
+      if (p < nc && i < sh.part[p].kept) li.all[at + i] = li.tops[p][i];
+      __syncthreads();
+      for (int c = tid; c < total; c += ST) {
+        const uint64_t k = li.all[c];
+        int above = 0;
+#pragma unroll 8
+        for (int i = 0; i < total; ++i) above += li.all[i] > k;
+        if (above < n) li.best[above] = k;
+      }
+    }
+  }
+  if (TOP) __syncthreads();
+  if (warp) return;
+  // one CTA a row: straight from its warps
+  const Part* parts = nc > 1 ? sh.part : sh.warp;
+  const Part w = lane < (nc > 1 ? nc : SW) ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
+  st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
+  ahead = __reduce_add_sync(0xffffffffu, w.ahead);
+  bad = __reduce_or_sync(0xffffffffu, w.bad);
+  const int kept = !TOP ? 0 : nc > 1 ? (int)__reduce_add_sync(0xffffffffu, w.kept) : sh.part[0].kept;
+  const int status = bad & SC_LATE ? SMP_ERR_TIMEOUT : !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
+                     : st.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
+  const bool ok = status == SMP_OK;
+  if (lane == 0) {
+    a.status[r] = status;
+    if (a.logprobs) a.logprobs[r] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, st, T);
+    if (a.entropy) a.entropy[r] = ok ? sc_entropy(st) : sc_nan();
+    if (a.rank) a.rank[r] = ok && t >= 0 ? ahead : -1;
+    if (a.stats) {
+      a.stats[2 * (size_t)r] = ok ? st.m : sc_nan();
+      a.stats[2 * (size_t)r + 1] = ok ? SC_LN2 * sc_log2_mass(st) : sc_nan();
+    }
+  }
+  if (TOP && lane < n) {
+    const uint64_t k = lane < kept ? li.best[lane] : 0ull;
+    a.top_ids[(size_t)r * n + lane] = ok && k ? key_id(k) : -1;
+    a.top_lp[(size_t)r * n + lane] = !ok ? sc_nan() : k ? sc_logprob(key_value(k), st, T) : -INFINITY;
+  }
+}
+
+template <int DT, int ST, bool LONG>
+int launch_score(const ScoreArgs& a, int nc, int seg, cudaStream_t st) {
+  constexpr int step = ST * (LONG ? 1 << SLNU : 8);
+  int gshift = 0;
+  while (((seg + step - 1) / step) >> gshift >= SBUCKETS) ++gshift;
+  if ((long long)a.B * nc > 0x7fffffffLL) return SMP_ERR_CAPACITY;
+  const auto kernel = a.n ? (a.bitmask ? score_kernel<DT, ST, LONG, true, true> : score_kernel<DT, ST, LONG, true, false>)
+                          : (a.bitmask ? score_kernel<DT, ST, LONG, false, true> : score_kernel<DT, ST, LONG, false, false>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * nc));
+  cfg.blockDim = dim3(ST);
+  cfg.stream = st;
+  if (LONG) {
+    cfg.dynamicSmemBytes = (ST * 16 << SLNU) * SSTAGES;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
+        cudaSuccess)
+      return SMP_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = nc > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+}
+
+// One CTA per row, or a cluster while the rows are fewer than SROWS for each SM and a
+// CTA has more than one chunk a warp.  Segments of one chunk a warp are short; a
+// row of one chunk for two warps takes a CTA of two, so that an SM holds many.
+template <int DT>
+int score_rows(const ScoreArgs& a, cudaStream_t st) {
+  const int sms = sc_sm_count();
+  if (sms < 1) return SMP_ERR_CUDA;
+  const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);  // whole ones, at most
+  if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 1, 64 * 8, st);
+  int nc = 1;
+  while (nc < SMAXC && (long long)a.B * nc * 2 <= (long long)SROWS_ * sms && vectors > nc * 256 * 8) nc *= 2;
+  const int seg = (vectors + nc - 1) / nc;
+  return seg <= 256 * 8 ? launch_score<DT, 256, false>(a, nc, seg, st) : launch_score<DT, 256, true>(a, nc, seg, st);
+}
+
+}  // namespace
+}  // namespace smp
