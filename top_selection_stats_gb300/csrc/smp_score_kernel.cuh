@@ -89,7 +89,7 @@ struct Word {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
   }
-  // the larger of each value; NaN loses
+  // the larger and the smaller of each value; NaN loses
   static __device__ __forceinline__ uint32_t max_num(uint32_t a, uint32_t b) {
     uint32_t r;
     if constexpr (DT == SMP_F32) asm("max.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -97,23 +97,37 @@ struct Word {
     else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
-  // A value to raise all smaller ones to without changing a sum: its weight
-  // is 0, it is finite and so is its d.  NONE where the type has none (and for
-  // binary32, where clamping d costs no more).
-  static __device__ __forceinline__ uint32_t floor_of(float m, float s) {
-    if constexpr (DT == SMP_F32) return NONE;
-    const float want = m - __fdividef(160.f, s);
-    uint32_t h;
-    float f;
+  static __device__ __forceinline__ uint32_t min_num(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == SMP_F32) asm("min.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if constexpr (DT == SMP_BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float bottom(uint32_t a) {
+    if constexpr (DT == SMP_F32) return __uint_as_float(a);
+    else if constexpr (DT == SMP_BF16) return fminf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    else return fminf(__half2float(__ushort_as_half((unsigned short)(a & 0xffffu))),
+                      __half2float(__ushort_as_half((unsigned short)(a >> 16))));
+  }
+  // 16-bit types: two values, each 1 where a > b, else 0; and their sums, exact up to 256
+  static __device__ __forceinline__ uint32_t above(uint32_t a, uint32_t b) {
     if constexpr (DT == SMP_BF16) {
-      h = __bfloat16_as_ushort(__float2bfloat16_rd(want));
-      f = __uint_as_float(h << 16);
+      const __nv_bfloat162 r = __hgt2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
     } else {
-      h = __half_as_ushort(__float2half_rd(want));
-      f = __half2float(__ushort_as_half((unsigned short)h));
+      const __half2 r = __hgt2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
     }
-    const float d = (f - m) * s;
-    return f > -INFINITY && d <= -150.f && d > -1e30f ? h * 0x00010001u : NONE;
+  }
+  static __device__ __forceinline__ uint32_t sum(uint32_t a, uint32_t b) {
+    if constexpr (DT == SMP_BF16) {
+      const __nv_bfloat162 r = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
   // word i of a vector with the values whose bit is 0 replaced by -inf
   static __device__ __forceinline__ uint32_t keep(uint32_t a, uint32_t bits, int i) {
@@ -187,7 +201,8 @@ struct Scratch {
 
 template <int DT, int ST, bool LONG, bool TOP, bool MASK>
 __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
-    score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift) {
+    score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift,
+                 const int r0, const bool rest) {
   const int nc = ST == 256 ? row_ctas : 1;  // CTAs of 64 threads have whole rows
   using TY = ScType<DT>;
   using raw = typename TY::raw;
@@ -203,7 +218,8 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
   static_assert(!LONG || sizeof(LI) <= (ST * 16 << SLNU) * SSTAGES, "the lists fit where the ring was");
   LI& li = *reinterpret_cast<LI*>(LONG ? ring_raw : sh.lists);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x / nc, rank_c = blockIdx.x % nc;
+  const int r = r0 + blockIdx.x / nc, rank_c = blockIdx.x % nc;
+  if (LONG) asm volatile("griddepcontrol.launch_dependents;");  // the launch for the rest, if there is one
   const raw* row = static_cast<const raw*>(a.logits) + (size_t)r * a.ld;
   const uint32_t* bm = MASK ? a.bitmask + (size_t)r * a.W : nullptr;
   auto legal = [&](int j) { return !MASK || ((__ldg(bm + (j >> 5)) >> (j & 31)) & 1u); };
@@ -216,14 +232,15 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
   const int v0 = min(f1, f0 + rank_c * seg), v1 = min(f1, v0 + seg);
   const uint4* src = reinterpret_cast<const uint4*>(row - lead);
   const int mine = v0 + warp * CV;  // this warp's first chunk; the next SW * CV further
+  const int chunks = max(0, (v1 - mine + SW * CV - 1) / (SW * CV));
 
   uint4 x[NU];
   uint32_t bits[MASK ? NW : 1];
   uint4* ring = reinterpret_cast<uint4*>(ring_raw) + warp * (SSTAGES * CV);
   uint64_t* full = sh.full + (LONG ? warp * SSTAGES : 0);
   auto fetch = [&](int i) {  // chunk i into its stage; what it does not fill holds nothing
+    if (i >= chunks) return;
     const int c = mine + i * (SW * CV), k = min(CV, v1 - c);
-    if (k <= 0) return;
     uint4* stage = ring + (i % SSTAGES) * CV;
     for (int e = k + lane; e < CV; e += 32) stage[e] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
     if (lane == 0) {
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
       if (v < v1) x[u] = load_vector(src + v);
     }
   }
-  if (MASK && mine < v1) load_bits(bits, bm, a.W, mine * VE - lead, CV * VE / 32);
+  if (MASK && chunks) load_bits(bits, bm, a.W, mine * VE - lead, CV * VE / 32);
 
   const float T = a.temperature ? a.temperature[r] : 1.f;
   const int t = a.targets ? a.targets[r] : -1;
@@ -263,6 +280,7 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
     const int j = lane < head ? lane : max(head, f1 * VE - lead) + lane - head;
     if (j < a.V && legal(j)) edge = j;
   }
+  const float xe = edge >= 0 ? TY::value(__ldg(row + edge)) : -INFINITY;
 
   // The lane's sums are relative to ref, which follows its largest value mx only
   // when that has left it by a factor of 2^SLAG: most chunks have a lane with
@@ -270,7 +288,14 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
   float ref = -INFINITY, mx = -INFINITY;
   f32x2 S2 = pair(0.f, 0.f), U2 = pair(0.f, 0.f);
   const f32x2 s2 = pair(s, s);
-  uint32_t low2 = WD::NONE;  // WD::floor_of(ref, s)
+  // 16-bit types: the target's logit in both halves, and the next smaller one, which
+  // is what a token before the target has to be above to come first
+  uint32_t same2 = 0u, less2 = 0u;
+  if constexpr (DT != SMP_F32) {
+    const uint32_t b = TY::store(xt), prev = b == 0u ? 0x8001u : b & 0x8000u ? b + 1 : b - 1;
+    same2 = b * 0x00010001u;
+    less2 = (xt == -INFINITY ? b : prev) * 0x00010001u;
+  }
   int ahead = 0, bad = 0;
   // x: the chunk whose first vector is c
   auto mask_chunk = [&]() {
@@ -307,26 +332,37 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
       U2 = mul2(fma2(S2, pair(d, d), U2), pair(e, e));
       S2 = mul2(S2, pair(e, e));
       if (raise) ref = top;
-      low2 = WD::floor_of(ref, s);
     }
     if (__any_sync(0xffffffffu, top >= xc)) {
+      uint32_t n2 = 0u;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         const int j0 = (c + u * 32 + lane) * VE - lead;
-        float f[VE];
-        sc_unpack<DT>(x[u], f);
+        if (DT == SMP_F32 || (j0 <= t && j0 + VE > t)) {
+          float f[VE];
+          sc_unpack<DT>(x[u], f);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) ahead += f[i] > xt || (f[i] == xt && j0 + i < t && xt > -INFINITY);
+          for (int i = 0; i < VE; ++i) ahead += f[i] > xt || (f[i] == xt && j0 + i < t && xt > -INFINITY);
+        } else if constexpr (DT != SMP_F32) {
+          const uint32_t b = j0 < t ? less2 : same2;
+          n2 = WD::sum(n2, WD::sum(WD::sum(WD::above(x[u].x, b), WD::above(x[u].y, b)),
+                                   WD::sum(WD::above(x[u].z, b), WD::above(x[u].w, b))));
+        }
       }
+      if constexpr (DT != SMP_F32) ahead += (int)(TY::value((raw)n2) + TY::value((raw)(n2 >> 16)));
     }
     const float base = ref == -INFINITY ? 0.f : -ref;
     const f32x2 mm = pair(base, base);
-    if (__all_sync(0xffffffffu, low2 != WD::NONE)) {
+    // no -inf, and none so low that d would be: nothing to clamp
+    uint32_t wm = x[0].x;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      wm = WD::min_num(wm, WD::min_num(WD::min_num(x[u].x, x[u].y), WD::min_num(x[u].z, x[u].w)));
+    if (__all_sync(0xffffffffu, (WD::bottom(wm) - ref) * s > -1.0e30f)) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         float f[VE];
-        sc_unpack<DT>(make_uint4(WD::max_num(x[u].x, low2), WD::max_num(x[u].y, low2),
-                                 WD::max_num(x[u].z, low2), WD::max_num(x[u].w, low2)), f);
+        sc_unpack<DT>(x[u], f);
 #pragma unroll
         for (int i = 0; i < VE; i += 2) {
           const f32x2 d = mul2(add2(pair(f[i], f[i + 1]), mm), s2);
@@ -356,22 +392,21 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
     }
   };
 
-  const int chunks = max(0, (v1 - mine + SW * CV - 1) / (SW * CV));  // of this warp
   if (LONG) {
     float bmax = -INFINITY;
     for (int i = 0; i < chunks; ++i) {
-      const int c = mine + i * (SW * CV), st = i % SSTAGES;
+      const int c = mine + i * (SW * CV), slot = i % SSTAGES;
       uint32_t next[MASK ? NW : 1];
       if (MASK && i + 1 < chunks) load_bits(next, bm, a.W, (c + SW * CV) * VE - lead, CV * VE / 32);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (i / SSTAGES) & 1, SWAIT))) {
-        // the copies behind it are given as long, then the CTA goes on without
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], (i / SSTAGES) & 1, SWAIT))) {
+        // the copies behind it are given as long, then the warp goes on without
         for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
           mbar_wait_bounded(&full[k % SSTAGES], (k / SSTAGES) & 1, SWAIT);
         bad = SC_LATE;
         break;
       }
 #pragma unroll
-      for (int u = 0; u < NU; ++u) x[u] = ring[st * CV + u * 32 + lane];
+      for (int u = 0; u < NU; ++u) x[u] = ring[slot * CV + u * 32 + lane];
       __syncwarp();
       fetch(i + SSTAGES);
       if (MASK) {
@@ -406,7 +441,6 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
     st.U = (b0 + b1 + (a0 + a1) * d) * c;
     if (!(mx < INFINITY)) bad |= SC_NONFINITE;
   }
-  const float xe = edge >= 0 ? TY::value(__ldg(row + edge)) : -INFINITY;
   if (edge >= 0) {
     if (!(xe < INFINITY)) bad |= SC_NONFINITE;
     sc_add(st, xe, s);
@@ -478,13 +512,24 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
         if (p < SCAND) li.cand[p] = k;
       }
     };
-    // the vector's values at or above the bound
+    // The vector's values at or above the bound.  Small code rather than
+    // unrolled: what runs once per row pays for its fetch.
     auto offer_vector = [&](const uint4& y, int j0, bool masked) {
+      const float least = key_value(max(bound, (uint64_t)0x00800000u << 32));  // any finite value, at least
       float f[VE];
       sc_unpack<DT>(y, f);
+      uint32_t hits = 0u;
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (order32(f[i]) >= (uint32_t)(bound >> 32) && (!masked || legal(j0 + i))) offer(f[i], j0 + i);
+      for (int i = 0; i < VE; ++i) hits |= f[i] >= least ? 1u << i : 0u;
+      while (hits) {
+        const int i = __ffs(hits) - 1, w = DT == SMP_F32 ? i : i >> 1;
+        hits &= hits - 1;
+        const uint32_t lo = w & 1 ? y.y : y.x, hi = w & 1 ? y.w : y.z, word = w & 2 ? hi : lo;
+        raw value;
+        if constexpr (DT == SMP_F32) value = __uint_as_float(word);
+        else value = (raw)(i & 1 ? word >> 16 : word);
+        if (!masked || legal(j0 + i)) offer(TY::value(value), j0 + i);
+      }
     };
     if constexpr (LONG) {
       const int buckets = (chunks + (1 << gshift) - 1) >> gshift;
@@ -507,28 +552,16 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
     while (true) {
       if (edge >= 0) offer(xe, edge);
 #pragma unroll 1
-      for (int i0 = tid; i0 < total; i0 += ST * 2) {
-        uint4 y[2];
-        int j0[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = i0 + h * ST;
-          y[h] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
-          j0[h] = 0;
-          if (i >= total) continue;
-          const int item = li.queue[i >> lv];
-          int v = v0 + item;
-          if constexpr (LONG) {
-            const int e = i & ((1 << lv) - 1), th = item % ST;
-            v = v0 + ((((item / ST) << gshift) + (e >> SLNU)) * SW + th / 32) * CV + (e % NU) * 32 + th % 32;
-          }
-          if (v < v1) {
-            y[h] = !LONG && i < SKEPT ? li.kept[i] : __ldg(src + v);
-            j0[h] = v * VE - lead;
-          }
+      for (int i = tid; i < total; i += ST) {
+        const int item = li.queue[i >> lv];
+        int v = v0 + item;
+        if constexpr (LONG) {
+          const int e = i & ((1 << lv) - 1), th = item % ST;
+          v = v0 + ((((item / ST) << gshift) + (e >> SLNU)) * SW + th / 32) * CV + (e % NU) * 32 + th % 32;
+          if (v >= v1) continue;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) offer_vector(y[h], j0[h], LONG || i0 + h * ST >= SKEPT);
+        const bool here = !LONG && i < SKEPT;
+        offer_vector(here ? li.kept[i] : __ldg(src + v), v * VE - lead, !here);
       }
       __syncthreads();
       found = sh.found;
@@ -608,18 +641,22 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
     a.top_ids[(size_t)r * n + lane] = ok && k ? key_id(k) : -1;
     a.top_lp[(size_t)r * n + lane] = !ok ? sc_nan() : k ? sc_logprob(key_value(k), st, T) : -INFINITY;
   }
+  // the rest's launch ends only after the one it started beside
+  if (rest && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Rows [r0, r0 + rows); rest: beside the launch before, on the SMs it leaves free.
 template <int DT, int ST, bool LONG>
-int launch_score(const ScoreArgs& a, int nc, int seg, cudaStream_t st) {
-  constexpr int step = ST * (LONG ? 1 << SLNU : 8);
+int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaStream_t st) {
+  constexpr int VE = DT == SMP_F32 ? 4 : 8, step = ST * (LONG ? 1 << SLNU : 8);
+  const int seg = (a.V / VE + nc - 1) / nc;
   int gshift = 0;
   while (((seg + step - 1) / step) >> gshift >= SBUCKETS) ++gshift;
-  if ((long long)a.B * nc > 0x7fffffffLL) return SMP_ERR_CAPACITY;
+  if ((long long)rows * nc > 0x7fffffffLL) return SMP_ERR_CAPACITY;
   const auto kernel = a.n ? (a.bitmask ? score_kernel<DT, ST, LONG, true, true> : score_kernel<DT, ST, LONG, true, false>)
                           : (a.bitmask ? score_kernel<DT, ST, LONG, false, true> : score_kernel<DT, ST, LONG, false, false>);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * nc));
+  cfg.gridDim = dim3((unsigned)(rows * nc));
   cfg.blockDim = dim3(ST);
   cfg.stream = st;
   if (LONG) {
@@ -628,29 +665,49 @@ int launch_score(const ScoreArgs& a, int nc, int seg, cudaStream_t st) {
         cudaSuccess)
       return SMP_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)nc;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  if (nc > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)nc;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (rest) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = nc > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, rest) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
 }
 
-// One CTA per row, or a cluster while the rows are fewer than SROWS for each SM and a
-// CTA has more than one chunk a warp.  Segments of one chunk a warp are short; a
-// row of one chunk for two warps takes a CTA of two, so that an SM holds many.
+// A row of one chunk for two warps takes a CTA of two, so that an SM holds many.
+// Longer rows take, as long as they come by the SMs' load, CTAs of four warps
+// (6 an SM): the fewer warps on a row, the less its start and end weigh.  What is left
+// takes CTAs of eight warps, a full load of rows at first, and the last rows in
+// clusters, as long as all their CTAs are resident at once and a warp has more
+// than a chunk; segments of one chunk a warp are short.  The second and
+// third launch run on what the one before leaves free.
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
   if (sms < 1) return SMP_ERR_CUDA;
+  constexpr int SHORT = 256 * 8;
   const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);  // whole ones, at most
-  if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 1, 64 * 8, st);
+  if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 0, a.B, 1, false, st);
+  if (vectors <= SHORT) return launch_score<DT, 256, false>(a, 0, a.B, 1, false, st);
+  const int slots = 3 * sms;
+  int done = 0, rc = SMP_OK;
+  const int many = (a.B - done) / slots * slots;
+  if (rc == SMP_OK && many) {
+    rc = launch_score<DT, 256, true>(a, done, many, 1, done > 0, st);
+    done += many;
+  }
+  if (rc != SMP_OK || done == a.B) return rc;
+  const int rows = a.B - done;
   int nc = 1;
-  while (nc < SMAXC && (long long)a.B * nc * 2 <= (long long)SROWS_ * sms && vectors > nc * 256 * 8) nc *= 2;
-  const int seg = (vectors + nc - 1) / nc;
-  return seg <= 256 * 8 ? launch_score<DT, 256, false>(a, nc, seg, st) : launch_score<DT, 256, true>(a, nc, seg, st);
+  while (nc < SMAXC && (long long)rows * nc * 2 <= 3 * sms && vectors > nc * SHORT) nc *= 2;
+  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, done, rows, nc, done > 0, st)
+                                          : launch_score<DT, 256, true>(a, done, rows, nc, done > 0, st);
 }
 
 }  // namespace

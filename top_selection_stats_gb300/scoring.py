@@ -12,24 +12,26 @@ import torch
 from .binding import _DTYPES, _check, load_library
 
 
-def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+_F32, _I32 = torch.float32, torch.int32
+# the current stream's handle without a Stream object (a microsecond less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _need(t, name, dev, dtype, shape):
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if t.dtype != dtype:
+def _need(t, name, index, dtype, shape):
+    if (t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name, dev, dtype, shape):
-    return None if t is None else _need(t, name, dev, dtype, shape)
+def _opt(t, name, index, dtype, shape):
+    return None if t is None else _need(t, name, index, dtype, shape)
 
 
 def _matrix(t, name, dtypes):
@@ -47,11 +49,11 @@ def _width(V, ld, name):
     return V
 
 
-def _launch(dev, fn, *args):
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, _stream(dev))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(dev))
+def _launch(index, fn, *args):
+    if torch.cuda.current_device() == index:
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
 
 
 def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=None, out=None,
@@ -68,30 +70,29 @@ def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=N
     L = lib or load_library()
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
-    dev = logits.device
-    f32, i32 = torch.float32, torch.int32
-    tg = _need(targets, "targets", dev, i32, (B,))
-    tp = _opt(temperature, "temperature", dev, f32, (B,))
-    bm = _opt(bitmask, "bitmask", dev, i32, (B, (V + 31) // 32))
+    dev = logits.get_device()
+    tg = _need(targets, "targets", dev, _I32, (B,))
+    tp = _opt(temperature, "temperature", dev, _F32, (B,))
+    bm = _opt(bitmask, "bitmask", dev, _I32, (B, (V + 31) // 32))
     if n_top < 0:
         raise ValueError("n_top must be >= 0")
     if out is None:
-        out = dict(logprobs=torch.empty(B, dtype=f32, device=dev),
-                   entropy=torch.empty(B, dtype=f32, device=dev),
-                   rank=torch.empty(B, dtype=i32, device=dev),
-                   stats=torch.empty((B, 2), dtype=f32, device=dev),
-                   status=torch.empty(B, dtype=i32, device=dev))
+        out = dict(logprobs=torch.empty(B, dtype=_F32, device=logits.device),
+                   entropy=torch.empty(B, dtype=_F32, device=logits.device),
+                   rank=torch.empty(B, dtype=_I32, device=logits.device),
+                   stats=torch.empty((B, 2), dtype=_F32, device=logits.device),
+                   status=torch.empty(B, dtype=_I32, device=logits.device))
         if n_top:
-            out["top_ids"] = torch.empty((B, n_top), dtype=i32, device=dev)
-            out["top_logprobs"] = torch.empty((B, n_top), dtype=f32, device=dev)
+            out["top_ids"] = torch.empty((B, n_top), dtype=_I32, device=logits.device)
+            out["top_logprobs"] = torch.empty((B, n_top), dtype=_F32, device=logits.device)
     rc = _launch(dev, L.smp_token_logprobs, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, bm,
-                 tp, tg, _need(out["logprobs"], "logprobs", dev, f32, (B,)),
-                 _need(out["entropy"], "entropy", dev, f32, (B,)),
-                 _need(out["rank"], "rank", dev, i32, (B,)),
-                 _need(out["stats"], "stats", dev, f32, (B, 2)),
-                 _need(out["status"], "status", dev, i32, (B,)), n_top,
-                 _need(out["top_ids"], "top_ids", dev, i32, (B, n_top)) if n_top else None,
-                 _need(out["top_logprobs"], "top_logprobs", dev, f32, (B, n_top)) if n_top else None)
+                 tp, tg, _need(out["logprobs"], "logprobs", dev, _F32, (B,)),
+                 _need(out["entropy"], "entropy", dev, _F32, (B,)),
+                 _need(out["rank"], "rank", dev, _I32, (B,)),
+                 _need(out["stats"], "stats", dev, _F32, (B, 2)),
+                 _need(out["status"], "status", dev, _I32, (B,)), n_top,
+                 _need(out["top_ids"], "top_ids", dev, _I32, (B, n_top)) if n_top else None,
+                 _need(out["top_logprobs"], "top_logprobs", dev, _F32, (B, n_top)) if n_top else None)
     _check(rc, "smp_token_logprobs")
     return out
 
@@ -107,8 +108,7 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
     L = lib or load_library()
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
-    dev = logits.device
-    f32, i32 = torch.float32, torch.int32
+    dev = logits.get_device()
     if grad_entropy is not None and entropy is None:
         raise ValueError("entropy is required with grad_entropy")
     if out is None:
@@ -116,13 +116,13 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
         if V < ld:
             out[:, V:].zero_()
     rc = _launch(dev, L.smp_token_logprobs_grad, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld,
-                 _opt(bitmask, "bitmask", dev, i32, (B, (V + 31) // 32)),
-                 _opt(temperature, "temperature", dev, f32, (B,)),
-                 _need(targets, "targets", dev, i32, (B,)),
-                 _need(stats, "stats", dev, f32, (B, 2)),
-                 _opt(entropy, "entropy", dev, f32, (B,)),
-                 _opt(grad_logprobs, "grad_logprobs", dev, f32, (B,)),
-                 _opt(grad_entropy, "grad_entropy", dev, f32, (B,)),
+                 _opt(bitmask, "bitmask", dev, _I32, (B, (V + 31) // 32)),
+                 _opt(temperature, "temperature", dev, _F32, (B,)),
+                 _need(targets, "targets", dev, _I32, (B,)),
+                 _need(stats, "stats", dev, _F32, (B, 2)),
+                 _opt(entropy, "entropy", dev, _F32, (B,)),
+                 _opt(grad_logprobs, "grad_logprobs", dev, _F32, (B,)),
+                 _opt(grad_entropy, "grad_entropy", dev, _F32, (B,)),
                  _need(out, "out", dev, logits.dtype, (B, ld)), ld)
     _check(rc, "smp_token_logprobs_grad")
     return out
@@ -138,34 +138,33 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
     L = lib or load_library()
     N, ldh = _matrix(hidden, "hidden", (torch.bfloat16, torch.float16))
     V, ldw = _matrix(weight, "weight", (torch.bfloat16, torch.float16))
-    dev = hidden.device
-    if weight.dtype != hidden.dtype or weight.device != dev:
+    dev = hidden.get_device()
+    if weight.dtype != hidden.dtype or weight.get_device() != dev:
         raise ValueError("hidden and weight must have one dtype and one device")
     if D is None and ldh != ldw:
         raise ValueError("hidden and weight must have rows of one length, or D given")
     D = _width(D, min(ldh, ldw), "D")
     if ldh % 8 or ldw % 8:
         raise ValueError("rows of hidden and weight must be a multiple of 8 values long")
-    f32, i32 = torch.float32, torch.int32
-    tg = _need(targets, "targets", dev, i32, (N,))
-    tp = _opt(temperature, "temperature", dev, f32, (N,))
+    tg = _need(targets, "targets", dev, _I32, (N,))
+    tp = _opt(temperature, "temperature", dev, _F32, (N,))
     if out is None:
-        out = dict(logprobs=torch.empty(N, dtype=f32, device=dev),
-                   entropy=torch.empty(N, dtype=f32, device=dev),
-                   stats=torch.empty((N, 2), dtype=f32, device=dev),
-                   status=torch.empty(N, dtype=i32, device=dev))
+        out = dict(logprobs=torch.empty(N, dtype=_F32, device=hidden.device),
+                   entropy=torch.empty(N, dtype=_F32, device=hidden.device),
+                   stats=torch.empty((N, 2), dtype=_F32, device=hidden.device),
+                   status=torch.empty(N, dtype=_I32, device=hidden.device))
     nbytes = L.smp_head_workspace(N, V)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
+    elif (workspace.dtype != torch.uint8 or workspace.get_device() != dev
           or not workspace.is_contiguous() or workspace.numel() < nbytes):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on {dev}")
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on cuda:{dev}")
     rc = _launch(dev, L.smp_head_logprobs, hidden.data_ptr(), ldh, weight.data_ptr(), ldw,
                  _DTYPES[hidden.dtype], N, V, D, tp, tg,
-                 _need(out["logprobs"], "logprobs", dev, f32, (N,)),
-                 _need(out["entropy"], "entropy", dev, f32, (N,)),
-                 _need(out["stats"], "stats", dev, f32, (N, 2)),
-                 _need(out["status"], "status", dev, i32, (N,)), workspace.data_ptr(),
+                 _need(out["logprobs"], "logprobs", dev, _F32, (N,)),
+                 _need(out["entropy"], "entropy", dev, _F32, (N,)),
+                 _need(out["stats"], "stats", dev, _F32, (N, 2)),
+                 _need(out["status"], "status", dev, _I32, (N,)), workspace.data_ptr(),
                  workspace.numel())
     _check(rc, "smp_head_logprobs")
     return out
