@@ -299,6 +299,11 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
   int ahead = 0, bad = 0;
   // x: the chunk whose first vector is c
   auto mask_chunk = [&]() {
+    uint32_t every = bits[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) every &= bits[w];
+    // all legal, as in most rows (a lane past the chunk's words holds 0)
+    if (__all_sync(0xffffffffu, every == 0xffffffffu || lane * 32 >= CV * VE)) return;
     bool whole = true;
     uint32_t b[NU];
 #pragma unroll
@@ -462,6 +467,7 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
       if (lane == k) mineq = top;
     }
     if (lane < q) sh.kth[warp * q + lane] = mineq;
+    for (int k = SW * q + tid; k < SFIRST; k += ST) sh.kth[k] = 0u;
     if (tid == 0) sh.queued = sh.found = 0;
   }
   if (nc > 1) {  // all CTAs of the row have started, and have their maxima in place
@@ -487,18 +493,20 @@ __global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
   }
 
   if constexpr (TOP) {
-    if (tid < SFIRST) {
-      const int each = SW * q, owner = tid / each;
-      uint32_t v = 0u;
-      if (owner < nc) v = nc > 1 ? *cg::this_cluster().map_shared_rank(&sh.kth[tid % each], owner) : sh.kth[tid];
-      li.first[tid] = v;
+    const uint32_t* firsts = sh.kth;
+    if (nc > 1) {
+      if (tid < SFIRST) {
+        const int each = SW * q, owner = tid / each;
+        li.first[tid] = owner < nc ? *cg::this_cluster().map_shared_rank(&sh.kth[tid % each], owner) : 0u;
+      }
+      firsts = li.first;
+      __syncthreads();
     }
-    __syncthreads();
     if (tid < SFIRST) {
-      const uint32_t v = li.first[tid];
+      const uint32_t v = firsts[tid];
       int above = 0;
 #pragma unroll 16
-      for (int i = 0; i < SFIRST; ++i) above += li.first[i] > v || (li.first[i] == v && i < tid);
+      for (int i = 0; i < SFIRST; ++i) above += firsts[i] > v || (firsts[i] == v && i < tid);
       if (above == n - 1) sh.low = max(v, 1u);  // 0: fewer than n; any legal value
     }
     __syncthreads();
