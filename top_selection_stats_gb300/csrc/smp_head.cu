@@ -2,13 +2,17 @@
 // the output head's weights (smp_head_logprobs): logits that only ever exist
 // as accumulators in tensor memory.
 //
-// head_kernel, one persistent CTA per SM, forms tiles of 128 states x BN tokens
-// with tcgen05.mma (16-bit operands, binary32 accumulators).  One thread feeds
-// a ring of TMA stages (64 values of D each, 128-byte swizzle), one thread
-// issues the products, and two groups of four warps, each with half of the
-// tile's columns, read finished accumulators into registers: a thread owns one
-// state's half row, folds it into a softmax state {m, S, U} and writes that to
-// the workspace with the target's logit.
+// head_kernel, one persistent CTA per SM, forms tiles of states x tokens with
+// tcgen05.mma (16-bit operands, binary32 accumulators): 256 x 256 on a pair of
+// CTAs, each staging its 128 states and half of the weights; up to 128 states,
+// where the stream of the weights is the bound, 128 x 128 on one CTA.  One
+// thread feeds a ring of TMA stages (64 values of D each, 128-byte swizzle),
+// one thread (of the pair) issues the products, and two groups of four warps,
+// each with half of the tile's columns, read finished accumulators into
+// registers: a thread owns one state's half row, folds it into a softmax state
+// {m, S, U} and writes that to the workspace with the target's logit.
+// 4096 x 128256 x 4096 bf16: 2453 us, 1.76 PFLOP/s under the power limit; on
+// single CTAs (128 x 256, half as much again from L2) 2563.
 //
 // The tensor cores' binary32 accumulation drops low bits instead of rounding:
 // over D = 4096 in one accumulator the logits were off by 5e-6 of their size.
@@ -40,17 +44,20 @@ constexpr int HTHREADS = (HEPI + 2) * 32;
 constexpr int HFLAGS = 1024;           // workspace: one word per CTA, then the tiles' states
 constexpr long long HWAIT = 4000000000ll;  // SM cycles: about two seconds
 
-template <int BN>
+template <int BN, bool PAIR>
 struct HeadShape {
+  static constexpr int BM = PAIR ? 2 * HBM : HBM;    // states per tile
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // tokens that a CTA stages
   static constexpr int A_BYTES = HBM * HBK * 2;
-  static constexpr int B_BYTES = BN * HBK * 2;
-  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int B_BYTES = B_ROWS * HBK * 2;
+  static constexpr int STAGES = 6;
   static constexpr int ACCS = 512 / BN;
   static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + 1024;  // + alignment
 };
 
 // Few states: the weights' stream is the bound, and narrower tiles spread it
-// more evenly over the SMs.
+// more evenly over the SMs.  More states: two CTAs on a tile of 256 x 256, so
+// that each stages half of the weights.
 int tile_tokens(int N) { return N <= HBM ? 128 : 256; }
 int tiles_of(int N, int V) { return (V + tile_tokens(N) - 1) / tile_tokens(N); }
 
@@ -103,28 +110,63 @@ __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
   while (!bar_try(b, parity) && clock64() - t0 <= HWAIT) {
   }
 }
-__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
+// The address of the pair's first CTA's `p`.
+__device__ __forceinline__ uint32_t first_addr(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+  return r;
+}
+__device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_addr(b)) : "memory");
+}
+// One box into this CTA's shared memory; its bytes count on `bar`, in a pair the first CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 // Shared-memory operand: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
 }
+// Arrives on `bar` when the products issued so far are done; in a pair on both CTAs'.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -146,16 +188,18 @@ __device__ __forceinline__ void acc_load(uint32_t addr, float (&v)[32]) {
       : "memory");
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(HTHREADS, 1)
     head_kernel(const HeadArgs a, const __grid_constant__ CUtensorMap map_h,
                 const __grid_constant__ CUtensorMap map_w, const uint32_t idesc, const uint32_t a_bytes) {
-  using SH = HeadShape<BN>;
+  using SH = HeadShape<BN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ HeadBars bars;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (a.N + HBM - 1) / HBM, vt = (a.V + BN - 1) / BN;
+  const int peer = PAIR ? blockIdx.x & 1 : 0;  // place in the pair; the first issues the products
+  const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, stride = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int mt = (a.N + SH::BM - 1) / SH::BM, vt = (a.V + BN - 1) / BN;
   const int kt = (a.D + HBK - 1) / HBK;
   const long long tiles = (long long)mt * vt;
   volatile int* fail = &bars.fail;
@@ -167,49 +211,64 @@ __global__ void __launch_bounds__(HTHREADS, 1)
     }
     for (int i = 0; i < SH::ACCS; ++i) {
       bar_init(&bars.acc_full[i], 1);
-      bar_init(&bars.acc_empty[i], HEPI);
+      bar_init(&bars.acc_empty[i], PAIR ? 2 * HEPI : HEPI);
     }
     bar_init(&bars.drain, 1);
     bars.fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == HEPI + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&bars.tmem)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&bars.tmem)),
+                   "r"(512u)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&bars.tmem)),
+                   "r"(512u)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     fence_before();
   }
   __syncthreads();
+  if constexpr (PAIR) {  // the other CTA's barriers and tensor memory are there
+    cluster_arrive();
+    cluster_wait();
+  }
   fence_after();
   const uint32_t tmem = bars.tmem;
 
   if (warp == HEPI) {  // copies
     if (lane == 0) {
       uint32_t i = 0;
-      for (long long tile = blockIdx.x; tile < tiles && !*fail; tile += gridDim.x) {
-        const int m0 = (int)(tile % mt) * HBM, v0 = (int)(tile / mt) * BN;
+      for (long long tile = first; tile < tiles && !*fail; tile += stride) {
+        const int m0 = (int)(tile % mt) * SH::BM + peer * HBM, v0 = (int)(tile / mt) * BN + peer * SH::B_ROWS;
         for (int k = 0; k < kt; ++k, ++i) {
           const uint32_t st = i % SH::STAGES, use = i / SH::STAGES;
           if (use && !bar_wait(&bars.empty[st], (use - 1) & 1, fail)) break;
           uint8_t* dst = ring + st * (SH::A_BYTES + SH::B_BYTES);
-          bar_expect(&bars.full[st], a_bytes + SH::B_BYTES);
-          tma_tile(dst, &map_h, k * HBK, m0, &bars.full[st]);
-          tma_tile(dst + SH::A_BYTES, &map_w, k * HBK, v0, &bars.full[st]);
+          if (!peer) bar_expect(&bars.full[st], (a_bytes + SH::B_BYTES) * (PAIR ? 2 : 1));
+          const uint32_t bar = PAIR ? first_addr(&bars.full[st]) : smem_addr(&bars.full[st]);
+          tma_tile<PAIR>(dst, &map_h, k * HBK, m0, bar);
+          tma_tile<PAIR>(dst + SH::A_BYTES, &map_w, k * HBK, v0, bar);
         }
       }
+      asm volatile("griddepcontrol.launch_dependents;");  // head_join may get ready
       // the last use of each stage: its products are done, or, when a wait ran
-      // out, its copy has at least landed, before the CTA ends
+      // out, its copies have at least landed, before the CTA ends (a pair's count on the
+      // first CTA's barriers, and neither ends before the other)
       for (uint32_t j = i > SH::STAGES ? i - SH::STAGES : 0; j < i; ++j) {
-        if (*fail || !bar_wait(&bars.empty[j % SH::STAGES], (j / SH::STAGES) & 1, fail))
-          bar_drain(&bars.full[j % SH::STAGES], (j / SH::STAGES) & 1);
+        const bool done = !*fail && bar_wait(&bars.empty[j % SH::STAGES], (j / SH::STAGES) & 1, fail);
+        if (!done && !peer) bar_drain(&bars.full[j % SH::STAGES], (j / SH::STAGES) & 1);
       }
     }
   } else if (warp == HEPI + 1) {  // products
-    if (lane == 0) {
+    if (lane == 0 && !peer) {
       uint32_t i = 0, sg = 0;
-      for (long long tile = blockIdx.x; tile < tiles && !*fail; tile += gridDim.x) {
+      for (long long tile = first; tile < tiles && !*fail; tile += stride) {
         for (int k0 = 0; k0 < kt && !*fail; k0 += HSEG, ++sg) {
           const uint32_t b = sg % SH::ACCS, use = sg / SH::ACCS;
           if (use && !bar_wait(&bars.acc_empty[b], (use - 1) & 1, fail)) break;
@@ -223,14 +282,14 @@ __global__ void __launch_bounds__(HTHREADS, 1)
             const uint64_t da = operand_desc(base), db = operand_desc(base + SH::A_BYTES);
 #pragma unroll
             for (int q = 0; q < HBK / 16; ++q)  // 16 values of D: 32 bytes further in the atom
-              mma(tmem + b * BN, da + 2 * q, db + 2 * q, idesc, k > k0 || q > 0);
-            mma_commit(&bars.empty[st]);
+              mma<PAIR>(tmem + b * BN, da + 2 * q, db + 2 * q, idesc, k > k0 || q > 0);
+            mma_commit<PAIR>(&bars.empty[st]);
           }
-          if (!*fail) mma_commit(&bars.acc_full[b]);
+          if (!*fail) mma_commit<PAIR>(&bars.acc_full[b]);
         }
       }
       if (*fail) {
-        mma_commit(&bars.drain);
+        mma_commit<PAIR>(&bars.drain);
         bar_drain(&bars.drain, 0);
       }
     }
@@ -238,7 +297,7 @@ __global__ void __launch_bounds__(HTHREADS, 1)
     constexpr int NC = BN / 2;
     uint32_t sg = 0;
     bool gone = false;
-    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (long long tile = first; tile < tiles; tile += stride) {
       float x[NC];
 #pragma unroll
       for (int j = 0; j < NC; ++j) x[j] = 0.f;
@@ -259,11 +318,14 @@ __global__ void __launch_bounds__(HTHREADS, 1)
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.acc_empty[b]);
+        if (lane == 0) {
+          if constexpr (PAIR) bar_arrive_first(&bars.acc_empty[b]);
+          else bar_arrive(&bars.acc_empty[b]);
+        }
       }
       if (gone) break;
       const int vtile = (int)(tile / mt), v0 = vtile * BN + c0;
-      const int row = (int)(tile % mt) * HBM + (warp & 3) * 32 + lane;
+      const int row = (int)(tile % mt) * SH::BM + peer * HBM + (warp & 3) * 32 + lane;
       const bool mine = row < a.N;
       const float T = mine && a.temperature ? a.temperature[row] : 1.f;
       const float s = sc_scale(sc_temperature_ok(T) ? T : 1.f);
@@ -302,9 +364,16 @@ __global__ void __launch_bounds__(HTHREADS, 1)
   __syncwarp();
   fence_before();
   __syncthreads();
+  if constexpr (PAIR) {  // neither CTA's memory is used by the other any more
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == HEPI + 1) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
   if (threadIdx.x == 0) reinterpret_cast<int*>(a.part)[blockIdx.x] = bars.fail;
 }
@@ -323,6 +392,7 @@ __global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, 
   Soft st{-INFINITY, 0.f, 0.f};
   float xt = -INFINITY;
   bool bad = false, late = false;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // head_kernel's states are complete
   for (int c = tid; c < ctas; c += HJOIN) late |= reinterpret_cast<const int*>(a.part)[c] != 0;
   const float4* part = a.part + HFLAGS / 4 + (size_t)row * parts;
   for (int c = tid; c < parts; c += 8 * HJOIN) {
@@ -393,30 +463,39 @@ bool tile_map(CUtensorMap* map, const void* base, int dtype, int rows, int D, lo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* ctas) {
-  using SH = HeadShape<BN>;
+  using SH = HeadShape<BN, PAIR>;
   // 8-row granules: of a state tile that N does not fill, only the rows there are are copied
   const int rows = a.N < HBM ? (a.N + 7) / 8 * 8 : HBM;
   CUtensorMap mh, mw;
   if (!tile_map(&mh, a.hidden, dtype, a.N, a.D, a.ldh, rows) ||
-      !tile_map(&mw, a.weight, dtype, a.V, a.D, a.ldw, BN))
+      !tile_map(&mw, a.weight, dtype, a.V, a.D, a.ldw, SH::B_ROWS))
     return SMP_ERR_CUDA;
   const uint32_t type = dtype == SMP_BF16 ? 1u : 0u;
-  // binary32 accumulators, both operands of `type` and K-major, N = BN, M = 128
+  // binary32 accumulators, both operands of `type` and K-major, N = BN, M = BM
   const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(BN >> 3) << 17) |
-                         ((uint32_t)(HBM >> 4) << 24);
-  if (cudaFuncSetAttribute(head_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) != cudaSuccess)
+                         ((uint32_t)(SH::BM >> 4) << 24);
+  if (cudaFuncSetAttribute(head_kernel<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) !=
+      cudaSuccess)
     return SMP_ERR_CUDA;
-  const long long tiles = (long long)((a.N + HBM - 1) / HBM) * ((a.V + BN - 1) / BN);
-  const int grid = (int)(tiles < sms ? tiles : sms);
+  constexpr int each = PAIR ? 2 : 1;
+  const long long tiles = (long long)((a.N + SH::BM - 1) / SH::BM) * ((a.V + BN - 1) / BN);
+  const int grid = (int)(tiles < sms / each ? tiles : sms / each) * each;
   *ctas = grid;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(HTHREADS);
   cfg.dynamicSmemBytes = SH::SMEM;
   cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, head_kernel<BN>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = each;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
              ? SMP_OK : SMP_ERR_CUDA;
 }
 
@@ -429,14 +508,19 @@ int64_t head_workspace(int N, int V) {
 int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st) {
   int ctas = 0;
   const int sms = sc_sm_count();
-  if (sms < 1 || sms > HFLAGS) return SMP_ERR_CUDA;
-  const int rc = tile_tokens(a.N) == 128 ? launch_head<128>(a, dtype, sms, st, &ctas)
-                                         : launch_head<256>(a, dtype, sms, st, &ctas);
+  if (sms < 2 || sms > HFLAGS) return SMP_ERR_CUDA;
+  const int rc = tile_tokens(a.N) == 128 ? launch_head<128, false>(a, dtype, sms, st, &ctas)
+                                         : launch_head<256, true>(a, dtype, sms, st, &ctas);
   if (rc != SMP_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.N);
   cfg.blockDim = dim3(HJOIN);
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, head_join, a, 2 * tiles_of(a.N, a.V), ctas) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
 }
 

@@ -29,12 +29,6 @@
 #include "smp_device.cuh"
 #include "smp_score.cuh"
 
-#ifndef SSTAGES_
-#define SSTAGES_ 2
-#define SLOCC_ 3
-#define SROWS_ 3
-#define SLNU_ 3
-#endif
 namespace smp {
 namespace {
 
@@ -42,9 +36,10 @@ constexpr int SBUCKETS = 8;   // buckets per thread, at most (long segments)
 constexpr int SCAND = 512;    // candidates ranked at a time
 constexpr int SMAXC = 8;      // CTAs of a row, at most
 constexpr int SKEPT = 64;      // short segments: vectors with candidates kept in shared memory
+constexpr int SROWS = 3;      // CTAs of 256 threads on an SM
 constexpr int SFIRST = 64;    // values the first bound is taken from
-constexpr int SLNU = SLNU_;
-constexpr int SSTAGES = SSTAGES_;    // ring: chunks in flight per warp
+constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
+constexpr int SSTAGES = 2;    // ring: chunks in flight per warp
 constexpr float SLAG = 8.f;
 constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
 
@@ -200,7 +195,7 @@ struct Scratch {
 };
 
 template <int DT, int ST, bool LONG, bool TOP, bool MASK>
-__global__ void __launch_bounds__(ST, (LONG ? SLOCC_ : 3) * 256 / ST)
+__global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift,
                  const int r0, const bool rest) {
   const int nc = ST == 256 ? row_ctas : 1;  // CTAs of 64 threads have whole rows
@@ -689,12 +684,12 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
 }
 
 // A row of one chunk for two warps takes a CTA of two, so that an SM holds many.
-// Longer rows take, as long as they come by the SMs' load, CTAs of four warps
-// (6 an SM): the fewer warps on a row, the less its start and end weigh.  What is left
-// takes CTAs of eight warps, a full load of rows at first, and the last rows in
-// clusters, as long as all their CTAs are resident at once and a warp has more
-// than a chunk; segments of one chunk a warp are short.  The second and
-// third launch run on what the one before leaves free.
+// Longer rows take CTAs of eight warps, one a row as long as the rows fill all SMs
+// (slots); the rows left after that a second launch, on what the first leaves
+// free, in clusters as large as still fit at once, while a warp has more than
+// a chunk.  Segments of one chunk a warp are short.  64 x 128256 bf16 with 20
+// alternatives: 13.6 us in clusters of 4, 20.7 of 8 (two rounds of CTAs); 1024
+// x 256000 f16 with 32: 122 us with the second launch, 134 without.
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
@@ -703,19 +698,15 @@ int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);  // whole ones, at most
   if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 0, a.B, 1, false, st);
   if (vectors <= SHORT) return launch_score<DT, 256, false>(a, 0, a.B, 1, false, st);
-  const int slots = 3 * sms;
-  int done = 0, rc = SMP_OK;
-  const int many = (a.B - done) / slots * slots;
-  if (rc == SMP_OK && many) {
-    rc = launch_score<DT, 256, true>(a, done, many, 1, done > 0, st);
-    done += many;
+  const int slots = SROWS * sms, many = a.B / slots * slots, rows = a.B - many;
+  if (many) {
+    const int rc = launch_score<DT, 256, true>(a, 0, many, 1, false, st);
+    if (rc != SMP_OK || !rows) return rc;
   }
-  if (rc != SMP_OK || done == a.B) return rc;
-  const int rows = a.B - done;
   int nc = 1;
-  while (nc < SMAXC && (long long)rows * nc * 2 <= 3 * sms && vectors > nc * SHORT) nc *= 2;
-  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, done, rows, nc, done > 0, st)
-                                          : launch_score<DT, 256, true>(a, done, rows, nc, done > 0, st);
+  while (nc < SMAXC && (long long)rows * nc * 2 <= slots && vectors > nc * SHORT) nc *= 2;
+  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, many, rows, nc, many > 0, st)
+                                          : launch_score<DT, 256, true>(a, many, rows, nc, many > 0, st);
 }
 
 }  // namespace
