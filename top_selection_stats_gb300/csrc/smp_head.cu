@@ -422,12 +422,13 @@ __global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, 
   const int status = late ? SMP_ERR_TIMEOUT : !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
                      : st.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
   const bool ok = status == SMP_OK;
+  const float L = sc_log_mass(st);
   a.status[row] = status;
-  if (a.logprobs) a.logprobs[row] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, st, T);
-  if (a.entropy) a.entropy[row] = ok ? sc_entropy(st) : sc_nan();
+  if (a.logprobs) a.logprobs[row] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, st.m, L, T);
+  if (a.entropy) a.entropy[row] = ok ? sc_entropy(st, L) : sc_nan();
   if (a.stats) {
     a.stats[2 * (size_t)row] = ok ? st.m : sc_nan();
-    a.stats[2 * (size_t)row + 1] = ok ? SC_LN2 * sc_log2_mass(st) : sc_nan();
+    a.stats[2 * (size_t)row + 1] = ok ? L : sc_nan();
   }
 }
 

@@ -128,14 +128,14 @@ __device__ __forceinline__ Soft sc_warp_merge(Soft a, float s) {
   return a;
 }
 
-// What a complete row's state gives.
-__device__ __forceinline__ float sc_log2_mass(const Soft& a) { return log2f(a.S); }
-__device__ __forceinline__ float sc_entropy(const Soft& a) {
-  return fmaxf(SC_LN2 * (log2f(a.S) - a.U / a.S), 0.f);
+// What a complete row's state gives: L = log of the mass relative to m, the
+// entropy, and the log probability of a value.
+__device__ __forceinline__ float sc_log_mass(const Soft& a) { return SC_LN2 * log2f(a.S); }
+__device__ __forceinline__ float sc_entropy(const Soft& a, float L) {
+  return fmaxf(L - SC_LN2 * (a.U / a.S), 0.f);
 }
-__device__ __forceinline__ float sc_logprob(float x, const Soft& a, float T) {
-  if (x == -INFINITY) return -INFINITY;
-  return fminf(__fdiv_rn(x - a.m, T) - SC_LN2 * log2f(a.S), 0.f);
+__device__ __forceinline__ float sc_logprob(float x, float m, float L, float T) {
+  return x == -INFINITY ? -INFINITY : fminf(__fdiv_rn(x - m, T) - L, 0.f);
 }
 
 template <int DT>

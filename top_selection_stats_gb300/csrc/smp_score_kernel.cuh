@@ -191,7 +191,8 @@ struct Scratch {
   uint32_t kth[SFIRST];
   uint64_t bound;
   uint32_t low;
-  int queued, found;
+  int queued, found, ok;
+  float m, log_mass;  // of the row, for the alternatives
 };
 
 template <int DT, int ST, bool LONG, bool TOP, bool MASK>
@@ -452,7 +453,8 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
   if (lane == 0) sh.warp[warp] = Part{st.m, st.S, st.U, ahead, bad, 0};
 
   const int n = a.n;
-  const int q = TOP ? min(SFIRST / (nc * SW), n) : 0;
+  // twice as many values as asked for, or as many as fit: hardly fewer make the bound loose
+  const int q = TOP ? min(min(SFIRST, 2 * n) / (nc * SW) + 1, min(SFIRST / (nc * SW), n)) : 0;
   if constexpr (TOP) {  // the warp's q largest lane maxima
     uint32_t key = order32(mx), mineq = 0u;
     for (int k = 0; k < q; ++k) {
@@ -472,7 +474,33 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
   } else {
     __syncthreads();
   }
+  // One warp: the row's results from the states of its parts.
+  auto finish = [&](const Part* parts, int count) {
+    const Part w = lane < count ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
+    const Soft b = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
+    const int before = __reduce_add_sync(0xffffffffu, w.ahead);
+    const int wrong = __reduce_or_sync(0xffffffffu, w.bad);
+    if (lane) return;
+    const int status = wrong & SC_LATE ? SMP_ERR_TIMEOUT : !valid ? SMP_ERR_INVALID_PARAM : wrong ? SMP_ERR_NONFINITE
+                       : b.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
+    const bool ok = status == SMP_OK;
+    const float L = sc_log_mass(b);
+    a.status[r] = status;
+    if (a.logprobs) a.logprobs[r] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, b.m, L, T);
+    if (a.entropy) a.entropy[r] = ok ? sc_entropy(b, L) : sc_nan();
+    if (a.rank) a.rank[r] = ok && t >= 0 ? before : -1;
+    if (a.stats) {
+      a.stats[2 * (size_t)r] = ok ? b.m : sc_nan();
+      a.stats[2 * (size_t)r + 1] = ok ? L : sc_nan();
+    }
+    if (TOP) {
+      sh.ok = ok;
+      sh.m = b.m;
+      sh.log_mass = L;
+    }
+  };
   Part* part = nc > 1 ? cg::this_cluster().map_shared_rank(&sh.part[rank_c], 0) : &sh.part[0];
+  if (TOP && nc == 1 && warp == SW - 1) finish(sh.warp, SW);  // while the others search
   if (nc > 1 && warp == SW - 1) {
     const Part w = lane < SW ? sh.warp[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
     st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
@@ -487,6 +515,7 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     }
   }
 
+  int kept = 0;
   if constexpr (TOP) {
     const uint32_t* firsts = sh.kth;
     if (nc > 1) {
@@ -591,7 +620,8 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
       for (int i = 0; i < found; ++i) above += li.cand[i] > k;
       if (above < n) to[above] = k;
     }
-    if (tid == 0) part->kept = min(found, n);
+    kept = min(found, n);
+    if (nc > 1 && tid == 0) part->kept = kept;
   }
 
   if (nc > 1) {  // the first CTA has everything; the others may go
@@ -608,6 +638,7 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
       }
       if (p < nc && i < sh.part[p].kept) li.all[at + i] = li.tops[p][i];
       __syncthreads();
+      if (warp == SW - 1) finish(sh.part, nc);
       for (int c = tid; c < total; c += ST) {
         const uint64_t k = li.all[c];
         int above = 0;
@@ -615,34 +646,17 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
         for (int i = 0; i < total; ++i) above += li.all[i] > k;
         if (above < n) li.best[above] = k;
       }
+      kept = min(total, n);
     }
   }
   if (TOP) __syncthreads();
   if (warp) return;
-  // one CTA a row: straight from its warps
-  const Part* parts = nc > 1 ? sh.part : sh.warp;
-  const Part w = lane < (nc > 1 ? nc : SW) ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0, 0, 0};
-  st = sc_warp_merge(Soft{w.m, w.S, w.U}, s);
-  ahead = __reduce_add_sync(0xffffffffu, w.ahead);
-  bad = __reduce_or_sync(0xffffffffu, w.bad);
-  const int kept = !TOP ? 0 : nc > 1 ? (int)__reduce_add_sync(0xffffffffu, w.kept) : sh.part[0].kept;
-  const int status = bad & SC_LATE ? SMP_ERR_TIMEOUT : !valid ? SMP_ERR_INVALID_PARAM : bad ? SMP_ERR_NONFINITE
-                     : st.m == -INFINITY ? SMP_ERR_EMPTY : SMP_OK;
-  const bool ok = status == SMP_OK;
-  if (lane == 0) {
-    a.status[r] = status;
-    if (a.logprobs) a.logprobs[r] = !ok ? sc_nan() : t < 0 ? 0.f : sc_logprob(xt, st, T);
-    if (a.entropy) a.entropy[r] = ok ? sc_entropy(st) : sc_nan();
-    if (a.rank) a.rank[r] = ok && t >= 0 ? ahead : -1;
-    if (a.stats) {
-      a.stats[2 * (size_t)r] = ok ? st.m : sc_nan();
-      a.stats[2 * (size_t)r + 1] = ok ? SC_LN2 * sc_log2_mass(st) : sc_nan();
-    }
-  }
+  if (!TOP) finish(nc > 1 ? sh.part : sh.warp, nc > 1 ? nc : SW);
   if (TOP && lane < n) {
-    const uint64_t k = lane < kept ? li.best[lane] : 0ull;
-    a.top_ids[(size_t)r * n + lane] = ok && k ? key_id(k) : -1;
-    a.top_lp[(size_t)r * n + lane] = !ok ? sc_nan() : k ? sc_logprob(key_value(k), st, T) : -INFINITY;
+    const uint64_t k = lane < kept && sh.ok ? li.best[lane] : 0ull;
+    a.top_ids[(size_t)r * n + lane] = k ? key_id(k) : -1;
+    a.top_lp[(size_t)r * n + lane] =
+        !sh.ok ? sc_nan() : k ? sc_logprob(key_value(k), sh.m, sh.log_mass, T) : -INFINITY;
   }
   // the rest's launch ends only after the one it started beside
   if (rest && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
