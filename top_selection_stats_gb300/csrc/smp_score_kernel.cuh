@@ -37,6 +37,7 @@ constexpr int SCAND = 512;    // candidates ranked at a time
 constexpr int SMAXC = 8;      // CTAs of a row, at most
 constexpr int SKEPT = 64;      // short segments: vectors with candidates kept in shared memory
 constexpr int SROWS = 3;      // CTAs of 256 threads on an SM
+constexpr int SSMALL = 16;    // and of 64
 constexpr int SFIRST = 64;    // values the first bound is taken from
 constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
 constexpr int SSTAGES = 2;    // ring: chunks in flight per warp
@@ -196,7 +197,7 @@ struct Scratch {
 };
 
 template <int DT, int ST, bool LONG, bool TOP, bool MASK>
-__global__ void __launch_bounds__(ST, SROWS * 256 / ST)
+__global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift,
                  const int r0, const bool rest) {
   const int nc = ST == 256 ? row_ctas : 1;  // CTAs of 64 threads have whole rows
@@ -227,8 +228,11 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
   const int f0 = lead ? 1 : 0, f1 = max(f0, (a.V + lead) / VE);
   const int v0 = min(f1, f0 + rank_c * seg), v1 = min(f1, v0 + seg);
   const uint4* src = reinterpret_cast<const uint4*>(row - lead);
-  const int mine = v0 + warp * CV;  // this warp's first chunk; the next SW * CV further
-  const int chunks = max(0, (v1 - mine + SW * CV - 1) / (SW * CV));
+  // this warp's first chunk; long: the next is SW * CV further; short: the segment in
+  // even parts of whole rounds of 32 vectors
+  const int part_v = LONG ? CV : (v1 - v0 + SW * 32 - 1) / (SW * 32) * 32;
+  const int mine = v0 + warp * part_v, stop = LONG ? v1 : min(v1, mine + part_v);
+  const int chunks = max(0, (stop - mine + SW * CV - 1) / (SW * CV));
 
   uint4 x[NU];
   uint32_t bits[MASK ? NW : 1];
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     for (int u = 0; u < NU; ++u) {
       const int v = mine + u * 32 + lane;
       x[u] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
-      if (v < v1) x[u] = load_vector(src + v);
+      if (v < stop) x[u] = load_vector(src + v);
     }
   }
   if (MASK && chunks) load_bits(bits, bm, a.W, mine * VE - lead, CV * VE / 32);
@@ -357,11 +361,14 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     // no -inf, and none so low that d would be: nothing to clamp
     uint32_t wm = x[0].x;
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int u = 0; u < NU; ++u) {
+      if (!LONG && u * 32 >= part_v) break;
       wm = WD::min_num(wm, WD::min_num(WD::min_num(x[u].x, x[u].y), WD::min_num(x[u].z, x[u].w)));
+    }
     if (__all_sync(0xffffffffu, (WD::bottom(wm) - ref) * s > -1.0e30f)) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
+        if (!LONG && u * 32 >= part_v) break;
         float f[VE];
         sc_unpack<DT>(x[u], f);
 #pragma unroll
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     } else {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
+        if (!LONG && u * 32 >= part_v) break;
         float f[VE];
         sc_unpack<DT>(x[u], f);
 #pragma unroll
@@ -570,10 +578,11 @@ __global__ void __launch_bounds__(ST, SROWS * 256 / ST)
     } else if (order32(mx) >= low) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
+        if (u * 32 >= part_v) break;
         const uint32_t wm = WD::max_num(WD::max_num(x[u].x, x[u].y), WD::max_num(x[u].z, x[u].w));
         if (order32(WD::top(wm)) >= low) {
           const int p = atomicAdd(&sh.queued, 1);
-          li.queue[p] = (unsigned short)(warp * CV + u * 32 + lane);
+          li.queue[p] = (unsigned short)(mine - v0 + u * 32 + lane);
           if (p < SKEPT) li.kept[p] = x[u];
         }
       }
@@ -697,13 +706,15 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, rest) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
 }
 
-// A row of one chunk for two warps takes a CTA of two, so that an SM holds many.
-// Longer rows take CTAs of eight warps, one a row as long as the rows fill all SMs
-// (slots); the rows left after that a second launch, on what the first leaves
-// free, in clusters as large as still fit at once, while a warp has more than
-// a chunk.  Segments of one chunk a warp are short.  64 x 128256 bf16 with 20
-// alternatives: 13.6 us in clusters of 4, 20.7 of 8 (two rounds of CTAs); 1024
-// x 256000 f16 with 32: 122 us with the second launch, 134 without.
+// Short rows, one chunk a warp, take CTAs of 2 or 4 warps, so that an SM holds many:
+// 4000 x 5000 bf16 with 5 alternatives 27.5 us in CTAs of 4 warps, 48.6 of 8.
+// Rows up to four times as long as 8 warps' chunks are taken by 4 warps while they
+// fill the SMs (3000 x 16000: 41 us, 46 with 8), others by 8: 4000 x 128256 with
+// 20 alternatives 193 us, 274 with 2.  The rows left when all others fill the SMs take a
+// second launch, on what the first leaves free, in clusters as large as still
+// fit at once, while a warp has more than a chunk: 1024 x 256000 f16 with 32
+// alternatives 122 us, 134 without; 64 x 128256 13.6 us in clusters of 4, 20.7 of 8
+// (two rounds of CTAs).
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
@@ -711,16 +722,27 @@ int score_rows(const ScoreArgs& a, cudaStream_t st) {
   constexpr int SHORT = 256 * 8;
   const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);  // whole ones, at most
   if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 0, a.B, 1, false, st);
-  if (vectors <= SHORT) return launch_score<DT, 256, false>(a, 0, a.B, 1, false, st);
-  const int slots = SROWS * sms, many = a.B / slots * slots, rows = a.B - many;
+  if (vectors <= 128 * 8) return launch_score<DT, 128, false>(a, 0, a.B, 1, false, st);
+  int done = 0;
+  if (vectors <= 8192) {
+    const int load = 2 * SROWS * sms;
+    done = a.B / load * load;
+    if (done) {
+      const int rc = launch_score<DT, 128, true>(a, 0, done, 1, false, st);
+      if (rc != SMP_OK || done == a.B) return rc;
+    }
+  }
+  if (vectors <= SHORT) return launch_score<DT, 256, false>(a, done, a.B - done, 1, done > 0, st);
+  const int slots = SROWS * sms, many = (a.B - done) / slots * slots, rows = a.B - done - many;
   if (many) {
-    const int rc = launch_score<DT, 256, true>(a, 0, many, 1, false, st);
+    const int rc = launch_score<DT, 256, true>(a, done, many, 1, done > 0, st);
     if (rc != SMP_OK || !rows) return rc;
+    done += many;
   }
   int nc = 1;
   while (nc < SMAXC && (long long)rows * nc * 2 <= slots && vectors > nc * SHORT) nc *= 2;
-  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, many, rows, nc, many > 0, st)
-                                          : launch_score<DT, 256, true>(a, many, rows, nc, many > 0, st);
+  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, done, rows, nc, done > 0, st)
+                                          : launch_score<DT, 256, true>(a, done, rows, nc, done > 0, st);
 }
 
 }  // namespace
