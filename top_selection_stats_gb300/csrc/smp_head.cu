@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(HTHREADS, 1)
     uint32_t sg = 0;
     bool gone = false;
     for (long long tile = first; tile < tiles; tile += stride) {
-      float x[NC];
+      f32x2 x2[NC / 2];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) x[j] = 0.f;
+      for (int j = 0; j < NC / 2; ++j) x2[j] = pair(0.f, 0.f);
       const int c0 = (warp >> 2) * NC;
       for (int k = 0; k < kt; k += HSEG, ++sg) {
         const uint32_t b = sg % SH::ACCS;
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(HTHREADS, 1)
           float v[32];
           acc_load(acc + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[c + j] += v[j];
+          for (int j = 0; j < 16; ++j) x2[c / 2 + j] = add2(x2[c / 2 + j], pair(v[2 * j], v[2 * j + 1]));
         }
         fence_before();
         __syncwarp();
@@ -330,6 +330,9 @@ __global__ void __launch_bounds__(HTHREADS, 1)
       const float T = mine && a.temperature ? a.temperature[row] : 1.f;
       const float s = sc_scale(sc_temperature_ok(T) ? T : 1.f);
       const int t = (mine && a.targets ? a.targets[row] : -1) - v0;  // the target's column, if any
+      float x[NC];
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j) unpair(x2[j], x[2 * j], x[2 * j + 1]);
       if (v0 + NC > a.V) {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
@@ -341,24 +344,44 @@ __global__ void __launch_bounds__(HTHREADS, 1)
         for (int j = 0; j < NC; ++j)
           if (t == j) xt = x[j];
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+      float m = x[0], low = x[0];
 #pragma unroll
-      for (int j = 4; j < NC; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-      const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const float mm = m == -INFINITY ? 0.f : m;
-      float S[4] = {0.f, 0.f, 0.f, 0.f}, U[4] = {0.f, 0.f, 0.f, 0.f};
-      bool nan = false;
+      for (int j = 1; j < NC; ++j) {
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(x[j]));
+        low = fminf(low, x[j]);
+      }
+      float S, U;
+      // no -inf or NaN, and nothing so low that its d would be -inf: nothing to clamp
+      if (__all_sync(0xffffffffu, (low - m) * s > -1.0e30f)) {
+        f32x2 S2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, U2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const f32x2 mm = pair(-m, -m), ss = pair(s, s);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const float z = (x[j] - mm) * s;
-        nan |= z != z;
-        const float d = fmaxf(z, SC_DMIN), e = sc_ex2(d);
-        S[j & 3] += e;
-        U[j & 3] = fmaf(e, d, U[j & 3]);
+        for (int j = 0; j < NC / 2; ++j) {
+          const f32x2 d = mul2(add2(pair(x[2 * j], x[2 * j + 1]), mm), ss);
+          float d0, d1;
+          unpair(d, d0, d1);
+          const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
+          S2[j & 1] = add2(S2[j & 1], e);
+          U2[j & 1] = fma2(e, d, U2[j & 1]);
+        }
+        float a0, a1;
+        unpair(add2(S2[0], S2[1]), a0, a1);
+        S = a0 + a1;
+        unpair(add2(U2[0], U2[1]), a0, a1);
+        U = a0 + a1;
+      } else {
+        const float mm = m == -INFINITY ? 0.f : m;
+        S = U = 0.f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const float d = fmaxf((x[j] - mm) * s, SC_DMIN), e = sc_ex2(d);
+          S += e;
+          U = fmaf(e, d, U);
+        }
       }
       if (mine)
-        a.part[HFLAGS / 4 + ((size_t)row * vt + vtile) * 2 + (warp >> 2)] = make_float4(
-            nan ? INFINITY : m, (S[0] + S[1]) + (S[2] + S[3]), (U[0] + U[1]) + (U[2] + U[3]), xt);
+        a.part[HFLAGS / 4 + ((size_t)row * vt + vtile) * 2 + (warp >> 2)] =
+            make_float4(m < INFINITY ? m : INFINITY, S, U, xt);
     }
   }
   __syncwarp();
