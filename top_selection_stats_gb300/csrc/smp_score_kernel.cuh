@@ -40,7 +40,14 @@ constexpr int SROWS = 3;      // CTAs of 256 threads on an SM
 constexpr int SSMALL = 16;    // and of 64
 constexpr int SFIRST = 64;    // values the first bound is taken from
 constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
-constexpr int SSTAGES = 2;    // ring: chunks in flight per warp
+// Ring: chunks a warp has in flight.  Two where the stream of bytes is the bound (4093
+// x 128256 bf16 without alternatives 151 us, 156 with one; 2000 x 128256 f32 154
+// and 161); one where the row's other work is, 16-bit logits with a mask or with
+// alternatives: what the ring leaves is cache for the mask and for what is read
+// again (512 x 151936 masked with 8: 52.6 us, 56.3 with two; 2000 x 40000 with 5:
+// 49.5 and 54.9).
+constexpr int ring_stages(int dt, bool top, bool mask) { return dt != SMP_F32 && (top || mask) ? 1 : 2; }
+constexpr int SMOST = 2;      // the larger of both
 constexpr float SLAG = 8.f;
 constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
 
@@ -185,7 +192,7 @@ template <int ST, bool LONG, bool TOP>
 struct Scratch {
   static constexpr int SW = ST / 32;
   alignas(16) unsigned char lists[TOP && !LONG ? sizeof(Lists<ST, LONG>) : 16];
-  uint64_t full[LONG ? SW * SSTAGES : 1];
+  uint64_t full[LONG ? SW * SMOST : 1];
   uint32_t bucket[LONG && TOP ? SBUCKETS * ST : 1];
   Part part[SMAXC];  // first CTA: the states of all
   Part warp[SW];
@@ -211,6 +218,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   constexpr int NW = (CV * VE / 32 + 31) / 32;  // mask words of a lane
   __shared__ __align__(16) Scratch<ST, LONG, TOP> sh;
   extern __shared__ __align__(128) uint8_t ring_raw[];
+  constexpr int SSTAGES = ring_stages(DT, TOP, MASK);
   using LI = Lists<ST, LONG>;
   static_assert(!LONG || sizeof(LI) <= (ST * 16 << SLNU) * SSTAGES, "the lists fit where the ring was");
   LI& li = *reinterpret_cast<LI*>(LONG ? ring_raw : sh.lists);
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     uint4* stage = ring + (i % SSTAGES) * CV;
     for (int e = k + lane; e < CV; e += 32) stage[e] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
     if (lane == 0) {
+      fence_proxy_async_smem();
       mbar_arrive_expect_tx(&full[i % SSTAGES], k * 16);
       bulk_g2s(stage, src + c, k * 16, &full[i % SSTAGES]);
     }
@@ -416,14 +425,14 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       }
 #pragma unroll
       for (int u = 0; u < NU; ++u) x[u] = ring[slot * CV + u * 32 + lane];
-      __syncwarp();
-      fetch(i + SSTAGES);
       if (MASK) {
         mask_chunk();
 #pragma unroll
         for (int w = 0; w < NW; ++w) bits[w] = next[w];
       }
       const float top = chunk_top();
+      __syncwarp();  // the stage has been read: every lane's values have gone into its top
+      fetch(i + SSTAGES);
       fold(c, top);
       if constexpr (TOP) {
         bmax = fmaxf(bmax, top);
@@ -686,7 +695,7 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
   cfg.blockDim = dim3(ST);
   cfg.stream = st;
   if (LONG) {
-    cfg.dynamicSmemBytes = (ST * 16 << SLNU) * SSTAGES;
+    cfg.dynamicSmemBytes = (ST * 16 << SLNU) * ring_stages(DT, a.n > 0, a.bitmask != nullptr);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
         cudaSuccess)
       return SMP_ERR_CUDA;
