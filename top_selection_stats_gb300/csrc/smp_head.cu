@@ -12,7 +12,8 @@
 // registers: a thread owns one state's half row, folds it into a softmax state
 // {m, S, U} and writes that to the workspace with the target's logit.
 // 4096 x 128256 x 4096 bf16: 2453 us, 1.76 PFLOP/s under the power limit; on
-// single CTAs (128 x 256, half as much again from L2) 2563.
+// single CTAs (128 x 256, half as much again from L2) 2563.  One state: 159.6
+// us, 6.6 TB/s of weights, with 10 stages of 32 state rows; 163.4 with 6 of 128.
 //
 // The tensor cores' binary32 accumulation drops low bits instead of rounding:
 // over D = 4096 in one accumulator the logits were off by 5e-6 of their size.
@@ -44,13 +45,16 @@ constexpr int HTHREADS = (HEPI + 2) * 32;
 constexpr int HFLAGS = 1024;           // workspace: one word per CTA, then the tiles' states
 constexpr long long HWAIT = 4000000000ll;  // SM cycles: about two seconds
 
-template <int BN, bool PAIR>
+// AR: rows of states that a stage has room for.  With AR < 128 the products read on into
+// the weights behind them: rows of the tile that no state has.
+template <int BN, bool PAIR, int AR>
 struct HeadShape {
   static constexpr int BM = PAIR ? 2 * HBM : HBM;    // states per tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // tokens that a CTA stages
-  static constexpr int A_BYTES = HBM * HBK * 2;
+  static constexpr int A_BYTES = AR * HBK * 2;
   static constexpr int B_BYTES = B_ROWS * HBK * 2;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = AR < HBM ? 10 : 6;
+  static_assert(A_BYTES + B_BYTES >= HBM * HBK * 2, "the last stage's products stay inside the ring");
   static constexpr int ACCS = 512 / BN;
   static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + 1024;  // + alignment
 };
@@ -62,7 +66,7 @@ int tile_tokens(int N) { return N <= HBM ? 128 : 256; }
 int tiles_of(int N, int V) { return (V + tile_tokens(N) - 1) / tile_tokens(N); }
 
 struct HeadBars {
-  uint64_t full[8], empty[8], acc_full[4], acc_empty[4], drain;
+  uint64_t full[10], empty[10], acc_full[4], acc_empty[4], drain;
   uint32_t tmem;
   int fail;
 };
@@ -188,11 +192,11 @@ __device__ __forceinline__ void acc_load(uint32_t addr, float (&v)[32]) {
       : "memory");
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, int AR>
 __global__ void __launch_bounds__(HTHREADS, 1)
     head_kernel(const HeadArgs a, const __grid_constant__ CUtensorMap map_h,
                 const __grid_constant__ CUtensorMap map_w, const uint32_t idesc, const uint32_t a_bytes) {
-  using SH = HeadShape<BN, PAIR>;
+  using SH = HeadShape<BN, PAIR, AR>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ HeadBars bars;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -487,11 +491,11 @@ bool tile_map(CUtensorMap* map, const void* base, int dtype, int rows, int D, lo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, int AR>
 int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* ctas) {
-  using SH = HeadShape<BN, PAIR>;
+  using SH = HeadShape<BN, PAIR, AR>;
   // 8-row granules: of a state tile that N does not fill, only the rows there are are copied
-  const int rows = a.N < HBM ? (a.N + 7) / 8 * 8 : HBM;
+  const int rows = a.N < AR ? (a.N + 7) / 8 * 8 : AR;
   CUtensorMap mh, mw;
   if (!tile_map(&mh, a.hidden, dtype, a.N, a.D, a.ldh, rows) ||
       !tile_map(&mw, a.weight, dtype, a.V, a.D, a.ldw, SH::B_ROWS))
@@ -500,7 +504,7 @@ int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* cta
   // binary32 accumulators, both operands of `type` and K-major, N = BN, M = BM
   const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(BN >> 3) << 17) |
                          ((uint32_t)(SH::BM >> 4) << 24);
-  if (cudaFuncSetAttribute(head_kernel<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) !=
+  if (cudaFuncSetAttribute(head_kernel<BN, PAIR, AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) !=
       cudaSuccess)
     return SMP_ERR_CUDA;
   constexpr int each = PAIR ? 2 : 1;
@@ -519,7 +523,7 @@ int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* cta
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR, AR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
              ? SMP_OK : SMP_ERR_CUDA;
 }
 
@@ -533,8 +537,9 @@ int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st) {
   int ctas = 0;
   const int sms = sc_sm_count();
   if (sms < 2 || sms > HFLAGS) return SMP_ERR_CUDA;
-  const int rc = tile_tokens(a.N) == 128 ? launch_head<128, false>(a, dtype, sms, st, &ctas)
-                                         : launch_head<256, true>(a, dtype, sms, st, &ctas);
+  const int rc = a.N <= 32 ? launch_head<128, false, 32>(a, dtype, sms, st, &ctas)
+                 : a.N <= HBM ? launch_head<128, false, HBM>(a, dtype, sms, st, &ctas)
+                              : launch_head<256, true, HBM>(a, dtype, sms, st, &ctas);
   if (rc != SMP_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.N);
