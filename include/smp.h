@@ -311,10 +311,10 @@ int smp_gumbel_sample(smp_handle h, const void* logits, smp_dtype dtype, int B, 
  * target outside [-1, V)), SMP_ERR_NONFINITE (NaN or +inf in a legal slot),
  * SMP_ERR_EMPTY (no legal token), SMP_ERR_TIMEOUT (a bounded device wait, about
  * two seconds, ran out).  Rows may start at any address that their type
- * allows; results do not depend on it, nor on the number of rows in a call.
- * Results are computed in binary32: a row's log-probabilities, entropy and L
- * are within a few 1e-6 of their exact values.  The calls use no atomics on
- * global memory: the same inputs give the same bits. */
+ * allows; unaligned ones are as fast.  Sums are in binary32 (typical errors: a
+ * few 1e-7 of a result).  The same call gives the same bits each time; the last
+ * bits of a row's sums may depend on its alignment and on how many rows
+ * share the call.  Ids, ranks and statuses are exact. */
 
 /* Log-probabilities of given tokens, with entropy, rank and the n most likely
  * alternatives ("Sampling system design" post, section on logprobs: an API
