@@ -41,11 +41,11 @@ constexpr int SSMALL = 16;    // and of 64
 constexpr int SFIRST = 64;    // values the first bound is taken from
 constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
 // Ring: chunks a warp has in flight.  Two where the stream of bytes is the bound (4093
-// x 128256 bf16 without alternatives 151 us, 156 with one; 2000 x 128256 f32 154
+// x 128256 bf16 without alternatives 152 us, 157 with one; 2000 x 128256 f32 155
 // and 161); one where the row's other work is, 16-bit logits with a mask or with
 // alternatives: what the ring leaves is cache for the mask and for what is read
-// again (512 x 151936 masked with 8: 52.6 us, 56.3 with two; 2000 x 40000 with 5:
-// 49.5 and 54.9).
+// again (512 x 151936 masked with 8: 53.7 us, 56.4 with two; 2000 x 40000 with 5:
+// 50.8 and 54.6).
 constexpr int ring_stages(int dt, bool top, bool mask) { return dt != SMP_F32 && (top || mask) ? 1 : 2; }
 constexpr int SMOST = 2;      // the larger of both
 constexpr float SLAG = 8.f;
@@ -716,14 +716,14 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
 }
 
 // Short rows, one chunk a warp, take CTAs of 2 or 4 warps, so that an SM holds many:
-// 4000 x 5000 bf16 with 5 alternatives 27.5 us in CTAs of 4 warps, 48.6 of 8.
+// 4000 x 5000 bf16 with 5 alternatives 27.6 us in CTAs of 4 warps, 33.0 of 8.
 // Rows up to four times as long as 8 warps' chunks are taken by 4 warps while they
-// fill the SMs (3000 x 16000: 41 us, 46 with 8), others by 8: 4000 x 128256 with
-// 20 alternatives 193 us, 274 with 2.  The rows left when all others fill the SMs take a
-// second launch, on what the first leaves free, in clusters as large as still
-// fit at once, while a warp has more than a chunk: 1024 x 256000 f16 with 32
-// alternatives 122 us, 134 without; 64 x 128256 13.6 us in clusters of 4, 20.7 of 8
-// (two rounds of CTAs).
+// fill the SMs (3000 x 16000 with 5: 38.7 us, 46.8 with 8), others by 8.  The rows left
+// when all others fill the SMs take a second launch, on what the first leaves
+// free, in clusters as large as still fit at once, while a warp has more than a
+// chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without the second
+// launch; 64 x 128256 bf16 with 20: 10.4 us in clusters of 4, 14.7 of 8 (two
+// rounds of CTAs).
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
