@@ -48,6 +48,10 @@ constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a ch
 // 50.8 and 54.6).
 constexpr int ring_stages(int dt, bool top, bool mask) { return dt != SMP_F32 && (top || mask) ? 1 : 2; }
 constexpr int SMOST = 2;      // the larger of both
+// Legal values of a lane in a chunk (of 64 or 32) that are taken one by one from the
+// stage: 4000 x 128256 bf16, a third of the rows with one token in twenty legal,
+// 184 us, 191 with every chunk taken whole; 512 x 151936 with 8 alternatives 50.2 and 53.7.
+constexpr int SFEW = 12;
 constexpr float SLAG = 8.f;
 constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
 
@@ -152,18 +156,20 @@ __device__ __forceinline__ uint4 load_vector(const uint4* p) {
   return q;
 }
 
-// The mask's bits for a chunk whose first element is j0 (>= 0), as words that start
-// there; word i is lane i % 32's [i / 32].  Elements past W words read as 0.
+// A chunk's words of the mask, shifted so that they start at the chunk's first value: p
+// is this lane's first of them, `left` how many the row has from the chunk's first on.
 template <int NW>
-__device__ __forceinline__ void load_bits(uint32_t (&w)[NW], const uint32_t* bm, int W, int j0, int words) {
+__device__ __forceinline__ void load_bits(uint32_t (&w)[NW], const uint32_t* p, int shift, int left) {
   const int lane = threadIdx.x & 31;
+  const bool inside = left > NW * 32;  // the word after the last is the row's too
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const int k = (j0 >> 5) + i * 32 + lane;
-    const bool in = i * 32 + lane < words;
-    const uint32_t lo = in && k < W ? __ldg(bm + k) : 0u;
-    const uint32_t hi = in && (j0 & 31) && k + 1 < W ? __ldg(bm + k + 1) : 0u;
-    w[i] = __funnelshift_r(lo, hi, j0 & 31);
+  for (int i = 0; i < NW; ++i) w[i] = inside || i * 32 + lane < left ? __ldg(p + i * 32) : 0u;
+  if (shift) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const uint32_t next = inside || i * 32 + lane + 1 < left ? __ldg(p + i * 32 + 1) : 0u;
+      w[i] = __funnelshift_r(w[i], next, shift);
+    }
   }
 }
 
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   constexpr int VE = 16 / (int)sizeof(raw);
   constexpr int NU = LONG ? 1 << SLNU : 8;  // vectors of a lane in a chunk
   constexpr int CV = 32 * NU;               // vectors of a chunk
-  constexpr int NW = (CV * VE / 32 + 31) / 32;  // mask words of a lane
+  constexpr int NW = CV * VE / 1024;        // mask words of a lane
   __shared__ __align__(16) Scratch<ST, LONG, TOP> sh;
   extern __shared__ __align__(128) uint8_t ring_raw[];
   constexpr int SSTAGES = ring_stages(DT, TOP, MASK);
@@ -274,7 +280,14 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       if (v < stop) x[u] = load_vector(src + v);
     }
   }
-  if (MASK && chunks) load_bits(bits, bm, a.W, mine * VE - lead, CV * VE / 32);
+  static_assert(NW * 32 == CV * VE / 32, "a chunk has whole words for each lane");
+  // the next chunk's words: their place in the row and its remainder
+  const int bit0 = mine * VE - lead;
+  const uint32_t* words = bm + (MASK ? (bit0 >> 5) + lane : 0);
+  int words_left = a.W - (bit0 >> 5);
+  if constexpr (MASK) {
+    if (chunks) load_bits(bits, words, bit0 & 31, words_left);
+  }
 
   const float T = a.temperature ? a.temperature[r] : 1.f;
   const int t = a.targets ? a.targets[r] : -1;
@@ -307,28 +320,40 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   }
   int ahead = 0, bad = 0;
   // x: the chunk whose first vector is c
-  auto mask_chunk = [&]() {
+  // The mask's bits of this lane's values in the chunk, VE for each vector: the
+  // first 32 in lo, the others in hi.
+  auto lane_bits = [&](uint32_t& lo, uint32_t& hi) {
+    uint32_t w[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) w[u] = __shfl_sync(0xffffffffu, bits[(u * VE) / 32], (u * VE + lane * VE / 32) & 31);
+    lo = hi = 0u;
+    if constexpr (VE == 8) {  // byte lane % 4 of each word
+      const uint32_t two = (lane & 3) * 0x11 + 0x40;
+#pragma unroll
+      for (int h = 0; h < NU; h += 4) {
+        const uint32_t b = __byte_perm(__byte_perm(w[h], w[h + 1], two), __byte_perm(w[h + 2], w[h + 3], two), 0x5410);
+        (h ? hi : lo) = b;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) lo |= ((w[u] >> (lane * VE & 31)) & ((1u << VE) - 1)) << (u * VE);
+    }
+  };
+  auto mask_chunk = [&](uint32_t lo, uint32_t hi) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const uint32_t b = (u * VE < 32 ? lo : hi) >> (u * VE & 31);
+      x[u].x = WD::keep(x[u].x, b, 0);
+      x[u].y = WD::keep(x[u].y, b, 1);
+      x[u].z = WD::keep(x[u].z, b, 2);
+      x[u].w = WD::keep(x[u].w, b, 3);
+    }
+  };
+  auto all_legal = [&]() {  // as in most rows
     uint32_t every = bits[0];
 #pragma unroll
     for (int w = 1; w < NW; ++w) every &= bits[w];
-    // all legal, as in most rows (a lane past the chunk's words holds 0)
-    if (__all_sync(0xffffffffu, every == 0xffffffffu || lane * 32 >= CV * VE)) return;
-    bool whole = true;
-    uint32_t b[NU];
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int word = u * (32 * VE / 32) + lane * VE / 32;  // VE bits of it
-      b[u] = __shfl_sync(0xffffffffu, bits[(u * VE) / 32], word & 31) >> (lane * VE & 31);
-      whole = whole && (b[u] & ((1u << VE) - 1)) == (1u << VE) - 1;
-    }
-    if (whole) return;  // as in most rows
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      x[u].x = WD::keep(x[u].x, b[u], 0);
-      x[u].y = WD::keep(x[u].y, b[u], 1);
-      x[u].z = WD::keep(x[u].z, b[u], 2);
-      x[u].w = WD::keep(x[u].w, b[u], 3);
-    }
+    return (bool)__all_sync(0xffffffffu, every == 0xffffffffu);
   };
   auto chunk_top = [&]() {
     uint32_t wm = WD::NONE;
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       wm = WD::max_nan(wm, WD::max_nan(WD::max_nan(x[u].x, x[u].y), WD::max_nan(x[u].z, x[u].w)));
     return WD::top(wm);
   };
-  auto fold = [&](int c, float top) {
+  auto follow = [&](float top) {  // mx and ref, before values up to top are added
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(top));
     const bool raise = (top - ref) * s > SLAG;
     if (__any_sync(0xffffffffu, raise)) {
@@ -347,6 +372,9 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       S2 = mul2(S2, pair(e, e));
       if (raise) ref = top;
     }
+  };
+  auto fold = [&](int c, float top) {
+    follow(top);
     if (__any_sync(0xffffffffu, top >= xc)) {
       uint32_t n2 = 0u;
 #pragma unroll
@@ -415,7 +443,11 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     for (int i = 0; i < chunks; ++i) {
       const int c = mine + i * (SW * CV), slot = i % SSTAGES;
       uint32_t next[MASK ? NW : 1];
-      if (MASK && i + 1 < chunks) load_bits(next, bm, a.W, (c + SW * CV) * VE - lead, CV * VE / 32);
+      if constexpr (MASK) {
+        words += SW * CV * VE / 32;
+        words_left -= SW * CV * VE / 32;
+        if (i + 1 < chunks) load_bits(next, words, bit0 & 31, words_left);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], (i / SSTAGES) & 1, SWAIT))) {
         // the copies behind it are given as long, then the warp goes on without
         for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
@@ -423,17 +455,56 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
         bad = SC_LATE;
         break;
       }
-#pragma unroll
-      for (int u = 0; u < NU; ++u) x[u] = ring[slot * CV + u * 32 + lane];
-      if (MASK) {
-        mask_chunk();
-#pragma unroll
-        for (int w = 0; w < NW; ++w) bits[w] = next[w];
+      float top = -INFINITY;
+      int most = SFEW + 1;  // legal values of a lane, at most
+      uint32_t lo = 0u, hi = 0u;
+      bool whole = true;
+      if constexpr (MASK) {
+        whole = all_legal();
+        if (!whole) {
+          lane_bits(lo, hi);
+          most = __reduce_max_sync(0xffffffffu, __popc(lo) + __popc(hi));
+        }
       }
-      const float top = chunk_top();
-      __syncwarp();  // the stage has been read: every lane's values have gone into its top
-      fetch(i + SSTAGES);
-      fold(c, top);
+      if (MASK && most <= SFEW) {  // few: taken one by one, straight from the stage
+        const raw* stage = reinterpret_cast<const raw*>(ring + slot * CV + lane);
+        const int first = (c + lane) * VE - lead;
+        float y[SFEW];
+#pragma unroll
+        for (int k = 0; k < SFEW; ++k) {
+          if (k >= most) break;
+          const bool low = lo != 0u;
+          const uint32_t b = low ? lo : hi;
+          const int e = (b ? __ffs(b) - 1 : 0) + (low ? 0 : 32);
+          const int at = (e & ~(VE - 1)) * 32 + (e & (VE - 1));
+          y[k] = b ? TY::value(stage[at]) : -INFINITY;
+          (low ? lo : hi) = b & (b - 1);
+          if (y[k] >= xc) ahead += y[k] > xt || (y[k] == xt && first + at < t && xt > -INFINITY);
+          asm("max.NaN.f32 %0, %1, %2;" : "=f"(top) : "f"(top), "f"(y[k]));
+        }
+        __syncwarp();  // the stage has been read
+        follow(top);
+        fetch(i + SSTAGES);
+        const float base = ref == -INFINITY ? 0.f : ref;
+        float S = 0.f, U = 0.f;
+#pragma unroll
+        for (int k = 0; k < SFEW; ++k) {
+          if (k >= most) break;
+          const float d = fmaxf((y[k] - base) * s, SC_DMIN), e = sc_ex2(d);
+          S += e;
+          U = fmaf(e, d, U);
+        }
+        S2 = add2(S2, pair(S, 0.f));
+        U2 = add2(U2, pair(U, 0.f));
+      } else {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) x[u] = ring[slot * CV + u * 32 + lane];
+        if (!whole) mask_chunk(lo, hi);
+        top = chunk_top();
+        __syncwarp();  // the stage has been read: every lane's values have gone into its top
+        fetch(i + SSTAGES);
+        fold(c, top);
+      }
       if constexpr (TOP) {
         bmax = fmaxf(bmax, top);
         if (((i + 1) & ((1 << gshift) - 1)) == 0 || i + 1 == chunks) {
@@ -441,9 +512,17 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
           bmax = -INFINITY;
         }
       }
+      if constexpr (MASK) {  // here, not earlier: the copy waits for the load
+#pragma unroll
+        for (int w = 0; w < NW; ++w) bits[w] = next[w];
+      }
     }
   } else if (chunks) {
-    if (MASK) mask_chunk();
+    if constexpr (MASK) {
+      uint32_t lo, hi;
+      lane_bits(lo, hi);
+      if (!all_legal()) mask_chunk(lo, hi);
+    }
     fold(mine, chunk_top());
   }
 

@@ -13,25 +13,36 @@ from .binding import _DTYPES, _check, load_library
 
 
 _F32, _I32 = torch.float32, torch.int32
-# the current stream's handle without a Stream object (a microsecond less a call)
+# the current stream's handle and device without the objects around them (a
+# microsecond less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _need(t, name, index, dtype, shape):
-    if (t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+def _need(t, name, index, dtype, n):
+    """The address of a contiguous tensor of n elements of dtype on device index."""
+    if t.get_device() == index and t.dtype is dtype and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name, index, dtype, shape):
-    return None if t is None else _need(t, name, index, dtype, shape)
+def _opt(t, name, index, dtype, n):
+    return None if t is None else _need(t, name, index, dtype, n)
+
+
+def _bitmask(t, index, B, V):
+    if t is None:
+        return None
+    if t.shape != (B, (V + 31) // 32):
+        raise ValueError("bitmask must be [B, ceil(V/32)]")
+    return _need(t, "bitmask", index, _I32, t.numel())
 
 
 def _matrix(t, name, dtypes):
@@ -50,7 +61,7 @@ def _width(V, ld, name):
 
 
 def _launch(index, fn, *args):
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return fn(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return fn(*args, _raw_stream(index))
@@ -71,9 +82,9 @@ def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=N
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
     dev = logits.get_device()
-    tg = _need(targets, "targets", dev, _I32, (B,))
-    tp = _opt(temperature, "temperature", dev, _F32, (B,))
-    bm = _opt(bitmask, "bitmask", dev, _I32, (B, (V + 31) // 32))
+    tg = _need(targets, "targets", dev, _I32, B)
+    tp = _opt(temperature, "temperature", dev, _F32, B)
+    bm = _bitmask(bitmask, dev, B, V)
     if n_top < 0:
         raise ValueError("n_top must be >= 0")
     if out is None:
@@ -86,13 +97,13 @@ def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=N
             out["top_ids"] = torch.empty((B, n_top), dtype=_I32, device=logits.device)
             out["top_logprobs"] = torch.empty((B, n_top), dtype=_F32, device=logits.device)
     rc = _launch(dev, L.smp_token_logprobs, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, bm,
-                 tp, tg, _need(out["logprobs"], "logprobs", dev, _F32, (B,)),
-                 _need(out["entropy"], "entropy", dev, _F32, (B,)),
-                 _need(out["rank"], "rank", dev, _I32, (B,)),
-                 _need(out["stats"], "stats", dev, _F32, (B, 2)),
-                 _need(out["status"], "status", dev, _I32, (B,)), n_top,
-                 _need(out["top_ids"], "top_ids", dev, _I32, (B, n_top)) if n_top else None,
-                 _need(out["top_logprobs"], "top_logprobs", dev, _F32, (B, n_top)) if n_top else None)
+                 tp, tg, _need(out["logprobs"], "logprobs", dev, _F32, B),
+                 _need(out["entropy"], "entropy", dev, _F32, B),
+                 _need(out["rank"], "rank", dev, _I32, B),
+                 _need(out["stats"], "stats", dev, _F32, 2 * B),
+                 _need(out["status"], "status", dev, _I32, B), n_top,
+                 _need(out["top_ids"], "top_ids", dev, _I32, B * n_top) if n_top else None,
+                 _need(out["top_logprobs"], "top_logprobs", dev, _F32, B * n_top) if n_top else None)
     _check(rc, "smp_token_logprobs")
     return out
 
@@ -115,15 +126,17 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
         out = torch.empty_like(logits)
         if V < ld:
             out[:, V:].zero_()
+    elif out.shape != logits.shape:
+        raise ValueError(f"out must have the logits' shape, got {list(out.shape)}")
     rc = _launch(dev, L.smp_token_logprobs_grad, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld,
-                 _opt(bitmask, "bitmask", dev, _I32, (B, (V + 31) // 32)),
-                 _opt(temperature, "temperature", dev, _F32, (B,)),
-                 _need(targets, "targets", dev, _I32, (B,)),
-                 _need(stats, "stats", dev, _F32, (B, 2)),
-                 _opt(entropy, "entropy", dev, _F32, (B,)),
-                 _opt(grad_logprobs, "grad_logprobs", dev, _F32, (B,)),
-                 _opt(grad_entropy, "grad_entropy", dev, _F32, (B,)),
-                 _need(out, "out", dev, logits.dtype, (B, ld)), ld)
+                 _bitmask(bitmask, dev, B, V),
+                 _opt(temperature, "temperature", dev, _F32, B),
+                 _need(targets, "targets", dev, _I32, B),
+                 _need(stats, "stats", dev, _F32, 2 * B),
+                 _opt(entropy, "entropy", dev, _F32, B),
+                 _opt(grad_logprobs, "grad_logprobs", dev, _F32, B),
+                 _opt(grad_entropy, "grad_entropy", dev, _F32, B),
+                 _need(out, "out", dev, logits.dtype, B * ld), ld)
     _check(rc, "smp_token_logprobs_grad")
     return out
 
@@ -146,8 +159,8 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
     D = _width(D, min(ldh, ldw), "D")
     if ldh % 8 or ldw % 8:
         raise ValueError("rows of hidden and weight must be a multiple of 8 values long")
-    tg = _need(targets, "targets", dev, _I32, (N,))
-    tp = _opt(temperature, "temperature", dev, _F32, (N,))
+    tg = _need(targets, "targets", dev, _I32, N)
+    tp = _opt(temperature, "temperature", dev, _F32, N)
     if out is None:
         out = dict(logprobs=torch.empty(N, dtype=_F32, device=hidden.device),
                    entropy=torch.empty(N, dtype=_F32, device=hidden.device),
@@ -161,10 +174,10 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on cuda:{dev}")
     rc = _launch(dev, L.smp_head_logprobs, hidden.data_ptr(), ldh, weight.data_ptr(), ldw,
                  _DTYPES[hidden.dtype], N, V, D, tp, tg,
-                 _need(out["logprobs"], "logprobs", dev, _F32, (N,)),
-                 _need(out["entropy"], "entropy", dev, _F32, (N,)),
-                 _need(out["stats"], "stats", dev, _F32, (N, 2)),
-                 _need(out["status"], "status", dev, _I32, (N,)), workspace.data_ptr(),
+                 _need(out["logprobs"], "logprobs", dev, _F32, N),
+                 _need(out["entropy"], "entropy", dev, _F32, N),
+                 _need(out["stats"], "stats", dev, _F32, 2 * N),
+                 _need(out["status"], "status", dev, _I32, N), workspace.data_ptr(),
                  workspace.numel())
     _check(rc, "smp_head_logprobs")
     return out
