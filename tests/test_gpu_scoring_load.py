@@ -103,3 +103,19 @@ def test_grad_skips_rows_without_gradient():
     torch.cuda.synchronize()
     assert not d[2].any() and torch.isfinite(d.float()).all() and d[0].any()
     assert np.isclose(d.float().sum(1).cpu().numpy(), 0.0, atol=0.05).all()  # sum of the gradient is 0
+
+
+@pytest.mark.parametrize("N", [1, 21, 100, 130])
+def test_head_does_not_depend_on_what_ran_before(N):
+    """Rows of a tile that no state has hold what earlier work left on the SM."""
+    c = T.head_case(N, 24514, 2764, "bf16", N, pad=4)
+    first = {k: v.clone() for k, v in T.check_head(c).items()}
+    other = T.head_case(256, 24514, 2764, "bf16", 9, pad=4)
+    for value in (float("nan"), float("inf"), 3e38, 0.0):
+        other["h"][:] = value
+        lib.head_logprobs(other["h"], other["w"], other["targets"], D=2764)
+        lib.head_logprobs(other["h"][:128].contiguous(), other["w"], other["targets"][:128].contiguous(), D=2764)
+        out = lib.head_logprobs(c["h"], c["w"], c["targets"], temperature=c["temperature"], D=c["D"])
+        torch.cuda.synchronize()
+        for k in first:
+            assert torch.equal(out[k].view(torch.int32), first[k].view(torch.int32)), (k, value)

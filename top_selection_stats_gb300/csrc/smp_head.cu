@@ -244,6 +244,9 @@ __global__ void __launch_bounds__(HTHREADS, 1)
   }
   fence_after();
   const uint32_t tmem = bars.tmem;
+  // The launch may overlap the end of the work before it on the stream: nothing of a
+  // caller's is read or written before that is complete.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == HEPI) {  // copies
     if (lane == 0) {
@@ -354,35 +357,36 @@ __global__ void __launch_bounds__(HTHREADS, 1)
         asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(x[j]));
         low = fminf(low, x[j]);
       }
-      float S, U;
-      // no -inf or NaN, and nothing so low that its d would be -inf: nothing to clamp
-      if (__all_sync(0xffffffffu, (low - m) * s > -1.0e30f)) {
-        f32x2 S2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, U2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        const f32x2 mm = pair(-m, -m), ss = pair(s, s);
-#pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          const f32x2 d = mul2(add2(pair(x[2 * j], x[2 * j + 1]), mm), ss);
-          float d0, d1;
-          unpair(d, d0, d1);
-          const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
-          S2[j & 1] = add2(S2[j & 1], e);
-          U2[j & 1] = fma2(e, d, U2[j & 1]);
+      // Usually there is no -inf or NaN, and nothing so low that its d would be -inf: nothing
+      // to clamp.  Both ways add the same values in the same order.  Lanes without a
+      // state hold what earlier work left and have no say.
+      const float mm = m == -INFINITY ? 0.f : m;
+      const f32x2 base = pair(-mm, -mm), ss = pair(s, s);
+      f32x2 S2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, U2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+      auto add = [&](int j, bool clamp) {
+        f32x2 d = mul2(add2(pair(x[2 * j], x[2 * j + 1]), base), ss);
+        float d0, d1;
+        unpair(d, d0, d1);
+        if (clamp) {
+          d0 = fmaxf(d0, SC_DMIN);
+          d1 = fmaxf(d1, SC_DMIN);
+          d = pair(d0, d1);
         }
-        float a0, a1;
-        unpair(add2(S2[0], S2[1]), a0, a1);
-        S = a0 + a1;
-        unpair(add2(U2[0], U2[1]), a0, a1);
-        U = a0 + a1;
+        const f32x2 e = pair(sc_ex2(d0), sc_ex2(d1));
+        S2[j & 1] = add2(S2[j & 1], e);
+        U2[j & 1] = fma2(e, d, U2[j & 1]);
+      };
+      if (__all_sync(0xffffffffu, !mine || (low - m) * s > -1.0e30f)) {
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) add(j, false);
       } else {
-        const float mm = m == -INFINITY ? 0.f : m;
-        S = U = 0.f;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          const float d = fmaxf((x[j] - mm) * s, SC_DMIN), e = sc_ex2(d);
-          S += e;
-          U = fmaf(e, d, U);
-        }
+        for (int j = 0; j < NC / 2; ++j) add(j, true);
       }
+      float a0, a1, b0, b1;
+      unpair(add2(S2[0], S2[1]), a0, a1);
+      unpair(add2(U2[0], U2[1]), b0, b1);
+      const float S = a0 + a1, U = b0 + b1;
       if (mine)
         a.part[HFLAGS / 4 + ((size_t)row * vt + vtile) * 2 + (warp >> 2)] =
             make_float4(m < INFINITY ? m : INFINITY, S, U, xt);
@@ -419,6 +423,7 @@ __global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, 
   Soft st{-INFINITY, 0.f, 0.f};
   float xt = -INFINITY;
   bool bad = false, late = false;
+  asm volatile("griddepcontrol.launch_dependents;");  // a next call's head_kernel may get ready
   asm volatile("griddepcontrol.wait;" ::: "memory");  // head_kernel's states are complete
   for (int c = tid; c < ctas; c += HJOIN) late |= reinterpret_cast<const int*>(a.part)[c] != 0;
   const float4* part = a.part + HFLAGS / 4 + (size_t)row * parts;
@@ -516,13 +521,15 @@ int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* cta
   cfg.blockDim = dim3(HTHREADS);
   cfg.dynamicSmemBytes = SH::SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = each;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = each;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
+  cfg.numAttrs = PAIR ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR, AR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
              ? SMP_OK : SMP_ERR_CUDA;
 }
