@@ -60,13 +60,6 @@ def _width(V, ld, name):
     return V
 
 
-def _launch(index, fn, *args):
-    if _current_device() == index:
-        return fn(*args, _raw_stream(index))
-    with torch.cuda.device(index):
-        return fn(*args, _raw_stream(index))
-
-
 def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=None, out=None,
                    lib=None):
     """smp_token_logprobs: per row of logits [B, V] (or [B, ld] with ``V``) the
@@ -82,6 +75,9 @@ def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=N
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
     dev = logits.get_device()
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, targets, temperature, bitmask, n_top, V, out, lib)
     tg = _need(targets, "targets", dev, _I32, B)
     tp = _opt(temperature, "temperature", dev, _F32, B)
     bm = _bitmask(bitmask, dev, B, V)
@@ -96,14 +92,15 @@ def token_logprobs(logits, targets, temperature=None, bitmask=None, n_top=0, V=N
         if n_top:
             out["top_ids"] = torch.empty((B, n_top), dtype=_I32, device=logits.device)
             out["top_logprobs"] = torch.empty((B, n_top), dtype=_F32, device=logits.device)
-    rc = _launch(dev, L.smp_token_logprobs, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, bm,
-                 tp, tg, _need(out["logprobs"], "logprobs", dev, _F32, B),
-                 _need(out["entropy"], "entropy", dev, _F32, B),
-                 _need(out["rank"], "rank", dev, _I32, B),
-                 _need(out["stats"], "stats", dev, _F32, 2 * B),
-                 _need(out["status"], "status", dev, _I32, B), n_top,
-                 _need(out["top_ids"], "top_ids", dev, _I32, B * n_top) if n_top else None,
-                 _need(out["top_logprobs"], "top_logprobs", dev, _F32, B * n_top) if n_top else None)
+    rc = L.smp_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, bm, tp, tg,
+                              _need(out["logprobs"], "logprobs", dev, _F32, B),
+                              _need(out["entropy"], "entropy", dev, _F32, B),
+                              _need(out["rank"], "rank", dev, _I32, B),
+                              _need(out["stats"], "stats", dev, _F32, 2 * B),
+                              _need(out["status"], "status", dev, _I32, B), n_top,
+                              _need(out["top_ids"], "top_ids", dev, _I32, B * n_top) if n_top else None,
+                              _need(out["top_logprobs"], "top_logprobs", dev, _F32, B * n_top) if n_top else None,
+                              _raw_stream(dev))
     _check(rc, "smp_token_logprobs")
     return out
 
@@ -120,6 +117,10 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
     dev = logits.get_device()
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return token_logprobs_grad(logits, targets, stats, grad_logprobs, entropy, grad_entropy,
+                                       temperature, bitmask, V, out, lib)
     if grad_entropy is not None and entropy is None:
         raise ValueError("entropy is required with grad_entropy")
     if out is None:
@@ -128,15 +129,15 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
             out[:, V:].zero_()
     elif out.shape != logits.shape:
         raise ValueError(f"out must have the logits' shape, got {list(out.shape)}")
-    rc = _launch(dev, L.smp_token_logprobs_grad, logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld,
-                 _bitmask(bitmask, dev, B, V),
-                 _opt(temperature, "temperature", dev, _F32, B),
-                 _need(targets, "targets", dev, _I32, B),
-                 _need(stats, "stats", dev, _F32, 2 * B),
-                 _opt(entropy, "entropy", dev, _F32, B),
-                 _opt(grad_logprobs, "grad_logprobs", dev, _F32, B),
-                 _opt(grad_entropy, "grad_entropy", dev, _F32, B),
-                 _need(out, "out", dev, logits.dtype, B * ld), ld)
+    rc = L.smp_token_logprobs_grad(logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld,
+                                   _bitmask(bitmask, dev, B, V),
+                                   _opt(temperature, "temperature", dev, _F32, B),
+                                   _need(targets, "targets", dev, _I32, B),
+                                   _need(stats, "stats", dev, _F32, 2 * B),
+                                   _opt(entropy, "entropy", dev, _F32, B),
+                                   _opt(grad_logprobs, "grad_logprobs", dev, _F32, B),
+                                   _opt(grad_entropy, "grad_entropy", dev, _F32, B),
+                                   _need(out, "out", dev, logits.dtype, B * ld), ld, _raw_stream(dev))
     _check(rc, "smp_token_logprobs_grad")
     return out
 
@@ -161,6 +162,9 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
     dev = hidden.get_device()
     if weight.dtype != hidden.dtype or weight.get_device() != dev:
         raise ValueError("hidden and weight must have one dtype and one device")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return head_logprobs(hidden, weight, targets, temperature, D, out, workspace, lib)
     if D is None and ldh != ldw:
         raise ValueError("hidden and weight must have rows of one length, or D given")
     D = _width(D, min(ldh, ldw), "D")
@@ -183,13 +187,13 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
     elif (workspace.dtype != torch.uint8 or workspace.get_device() != dev
           or not workspace.is_contiguous() or workspace.numel() < nbytes):
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on cuda:{dev}")
-    rc = _launch(dev, L.smp_head_logprobs, hidden.data_ptr(), ldh, weight.data_ptr(), ldw,
-                 _DTYPES[hidden.dtype], N, V, D, tp, tg,
-                 _need(out["logprobs"], "logprobs", dev, _F32, N),
-                 _need(out["entropy"], "entropy", dev, _F32, N),
-                 _need(out["stats"], "stats", dev, _F32, 2 * N),
-                 _need(out["status"], "status", dev, _I32, N), workspace.data_ptr(),
-                 workspace.numel())
+    rc = L.smp_head_logprobs(hidden.data_ptr(), ldh, weight.data_ptr(), ldw,
+                             _DTYPES[hidden.dtype], N, V, D, tp, tg,
+                             _need(out["logprobs"], "logprobs", dev, _F32, N),
+                             _need(out["entropy"], "entropy", dev, _F32, N),
+                             _need(out["stats"], "stats", dev, _F32, 2 * N),
+                             _need(out["status"], "status", dev, _I32, N), workspace.data_ptr(),
+                             workspace.numel(), _raw_stream(dev))
     _check(rc, "smp_head_logprobs")
     return out
 
