@@ -119,3 +119,51 @@ def test_head_does_not_depend_on_what_ran_before(N):
         torch.cuda.synchronize()
         for k in first:
             assert torch.equal(out[k].view(torch.int32), first[k].view(torch.int32)), (k, value)
+
+
+@pytest.mark.parametrize("B,V", [(1, 128256), (64, 32000), (300, 5003), (300, 300), (600, 20000)])
+def test_calls_follow_the_work_before_them(B, V):
+    """Launches may start under the end of earlier work; what it writes is what they read.
+    Each turn overwrites the logits, scores them, replaces them by their gradient and
+    scores that, with nothing in between that waits."""
+    g = torch.ones(B, device="cuda")
+    sets = [T.make(B, V, "bf16", k, temps=[1.0]) for k in range(3)]
+    want = []
+    for c in sets:
+        f = T.run(c, 5)
+        x = c["x"].clone()
+        lib.token_logprobs_grad(x, c["targets"], f["stats"], grad_logprobs=g, out=x)
+        torch.cuda.synchronize()
+        f2 = T.run(dict(c, x=x), 5)
+        want.append({k: v.clone() for k, v in f.items()} | {"2" + k: v.clone() for k, v in f2.items()})
+    x = torch.empty_like(sets[0]["x"])
+    got = []
+    for turn in range(30):
+        c = sets[turn % 3]
+        x.copy_(c["x"])
+        f = lib.token_logprobs(x, c["targets"], n_top=5)
+        lib.token_logprobs_grad(x, c["targets"], f["stats"], grad_logprobs=g, out=x)
+        f2 = lib.token_logprobs(x, c["targets"], n_top=5)
+        x.fill_(7.0)
+        got.append(f | {"2" + k: v for k, v in f2.items()})
+    torch.cuda.synchronize()
+    for turn, r in enumerate(got):
+        for k, v in want[turn % 3].items():
+            assert torch.equal(r[k].view(torch.int32), v.view(torch.int32)), (turn, k)
+
+
+def test_head_follows_the_work_before_it():
+    c = [T.head_case(20, 5000, 512, "bf16", k) for k in range(3)]
+    want = [{k: v.clone() for k, v in T.check_head(x).items()} for x in c]
+    h, w = torch.empty_like(c[0]["h"]), torch.empty_like(c[0]["w"])
+    got = []
+    for turn in range(30):
+        x = c[turn % 3]
+        h.copy_(x["h"])
+        w.copy_(x["w"])
+        got.append(lib.head_logprobs(h, w, x["targets"], temperature=x["temperature"]))
+        w.zero_()
+    torch.cuda.synchronize()
+    for turn, r in enumerate(got):
+        for k, v in want[turn % 3].items():
+            assert torch.equal(r[k].view(torch.int32), v.view(torch.int32)), (turn, k)

@@ -150,7 +150,7 @@ struct Word {
 // A vector of a row that is read once.
 __device__ __forceinline__ uint4 load_vector(const uint4* p) {
   uint4 q;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
                : "l"(p));
   return q;
@@ -163,11 +163,11 @@ __device__ __forceinline__ void load_bits(uint32_t (&w)[NW], const uint32_t* p, 
   const int lane = threadIdx.x & 31;
   const bool inside = left > NW * 32;  // the word after the last is the row's too
 #pragma unroll
-  for (int i = 0; i < NW; ++i) w[i] = inside || i * 32 + lane < left ? __ldg(p + i * 32) : 0u;
+  for (int i = 0; i < NW; ++i) w[i] = inside || i * 32 + lane < left ? p[i * 32] : 0u;
   if (shift) {
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      const uint32_t next = inside || i * 32 + lane + 1 < left ? __ldg(p + i * 32 + 1) : 0u;
+      const uint32_t next = inside || i * 32 + lane + 1 < left ? p[i * 32 + 1] : 0u;
       w[i] = __funnelshift_r(w[i], next, shift);
     }
   }
@@ -212,7 +212,7 @@ struct Scratch {
 template <int DT, int ST, bool LONG, bool TOP, bool MASK>
 __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     score_kernel(const ScoreArgs a, const int row_ctas, const int seg, const int gshift,
-                 const int r0, const bool rest) {
+                 const int r0, const bool more) {
   const int nc = ST == 256 ? row_ctas : 1;  // CTAs of 64 threads have whole rows
   using TY = ScType<DT>;
   using raw = typename TY::raw;
@@ -230,10 +230,9 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   LI& li = *reinterpret_cast<LI*>(LONG ? ring_raw : sh.lists);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = r0 + blockIdx.x / nc, rank_c = blockIdx.x % nc;
-  if (LONG) asm volatile("griddepcontrol.launch_dependents;");  // the launch for the rest, if there is one
   const raw* row = static_cast<const raw*>(a.logits) + (size_t)r * a.ld;
   const uint32_t* bm = MASK ? a.bitmask + (size_t)r * a.W : nullptr;
-  auto legal = [&](int j) { return !MASK || ((__ldg(bm + (j >> 5)) >> (j & 31)) & 1u); };
+  auto legal = [&](int j) { return !MASK || ((bm[j >> 5] >> (j & 31)) & 1u); };
 
   // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
   // [f0, f1) lie inside the row; what is left at its ends, fewer than 2 VE
@@ -263,13 +262,20 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       bulk_g2s(stage, src + c, k * 16, &full[i % SSTAGES]);
     }
   };
+  if (LONG && lane == 0) {
+    for (int i = 0; i < SSTAGES; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  // A call of one launch gets ready under the end of the work before it on the stream
+  // (8 x 128256: 4.3 to 4.0 us): nothing of a caller's is read or written before that
+  // is complete.  It lets no other start early, whose CTAs would take their places
+  // while these still have theirs, unevenly (256 x 128256 with 20 top: 26.6 us, not
+  // 21.6).  Of a call of two launches the second starts once all CTAs of the first have.
+  if (r0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (more) asm volatile("griddepcontrol.launch_dependents;");
   if (LONG) {
-    if (lane == 0) {
-      for (int i = 0; i < SSTAGES; ++i) mbar_init(&full[i], 1);
-      fence_mbar_init();
-      fence_proxy_async_smem();
-    }
-    __syncwarp();
     for (int i = 0; i < SSTAGES; ++i) fetch(i);
     __syncwarp();
   } else {  // on its way before the row's parameters are waited for
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   const int t = a.targets ? a.targets[r] : -1;
   const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
   const float s = sc_scale(valid ? T : 1.f);
-  const float xt = valid && t >= 0 && legal(t) ? TY::value(__ldg(row + t)) : -INFINITY;
+  const float xt = valid && t >= 0 && legal(t) ? TY::value(row[t]) : -INFINITY;
   // counted: values at or above this (nothing without a target or a rank)
   const float xc = valid && t >= 0 && a.rank ? xt : INFINITY;
   int edge = -1;
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     const int j = lane < head ? lane : max(head, f1 * VE - lead) + lane - head;
     if (j < a.V && legal(j)) edge = j;
   }
-  const float xe = edge >= 0 ? TY::value(__ldg(row + edge)) : -INFINITY;
+  const float xe = edge >= 0 ? TY::value(row[edge]) : -INFINITY;
 
   // The lane's sums are relative to ref, which follows its largest value mx only
   // when that has left it by a factor of 2^SLAG: most chunks have a lane with
@@ -690,7 +696,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
           if (v >= v1) continue;
         }
         const bool here = !LONG && i < SKEPT;
-        offer_vector(here ? li.kept[i] : __ldg(src + v), v * VE - lead, !here);
+        offer_vector(here ? li.kept[i] : src[v], v * VE - lead, !here);
       }
       __syncthreads();
       found = sh.found;
@@ -755,13 +761,14 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     a.top_lp[(size_t)r * n + lane] =
         !sh.ok ? sc_nan() : k ? sc_logprob(key_value(k), sh.m, sh.log_mass, T) : -INFINITY;
   }
-  // the rest's launch ends only after the one it started beside
-  if (rest && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the second launch ends only after the one it started beside
+  if (r0 && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Rows [r0, r0 + rows); rest: beside the launch before, on the SMs it leaves free.
+// Rows [r0, r0 + rows).
 template <int DT, int ST, bool LONG>
-int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaStream_t st) {
+int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) {
+  const bool more = r0 + rows < a.B;
   constexpr int VE = DT == SMP_F32 ? 4 : 8, step = ST * (LONG ? 1 << SLNU : 8);
   const int seg = (a.V / VE + nc - 1) / nc;
   int gshift = 0;
@@ -786,12 +793,12 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs++].val.clusterDim.z = 1;
   }
-  if (rest) {
+  if (r0 || !more) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, rest) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, more) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
 }
 
 // Short rows, one chunk a warp, take CTAs of 2 or 4 warps, so that an SM holds many:
@@ -801,7 +808,7 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, bool rest, cudaSt
 // when all others fill the SMs take a second launch, on what the first leaves
 // free, in clusters as large as still fit at once, while a warp has more than a
 // chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without the second
-// launch; 64 x 128256 bf16 with 20: 10.4 us in clusters of 4, 14.7 of 8 (two
+// launch; 64 x 128256 bf16 with 20: 10.1 us in clusters of 4, 14.7 of 8 (two
 // rounds of CTAs).
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
@@ -809,28 +816,28 @@ int score_rows(const ScoreArgs& a, cudaStream_t st) {
   if (sms < 1) return SMP_ERR_CUDA;
   constexpr int SHORT = 256 * 8;
   const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);  // whole ones, at most
-  if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 0, a.B, 1, false, st);
-  if (vectors <= 128 * 8) return launch_score<DT, 128, false>(a, 0, a.B, 1, false, st);
+  if (vectors <= 64 * 8) return launch_score<DT, 64, false>(a, 0, a.B, 1, st);
+  if (vectors <= 128 * 8) return launch_score<DT, 128, false>(a, 0, a.B, 1, st);
   int done = 0;
   if (vectors <= 8192) {
     const int load = 2 * SROWS * sms;
     done = a.B / load * load;
     if (done) {
-      const int rc = launch_score<DT, 128, true>(a, 0, done, 1, false, st);
+      const int rc = launch_score<DT, 128, true>(a, 0, done, 1, st);
       if (rc != SMP_OK || done == a.B) return rc;
     }
   }
-  if (vectors <= SHORT) return launch_score<DT, 256, false>(a, done, a.B - done, 1, done > 0, st);
+  if (vectors <= SHORT) return launch_score<DT, 256, false>(a, done, a.B - done, 1, st);
   const int slots = SROWS * sms, many = (a.B - done) / slots * slots, rows = a.B - done - many;
   if (many) {
-    const int rc = launch_score<DT, 256, true>(a, done, many, 1, done > 0, st);
+    const int rc = launch_score<DT, 256, true>(a, done, many, 1, st);
     if (rc != SMP_OK || !rows) return rc;
     done += many;
   }
   int nc = 1;
   while (nc < SMAXC && (long long)rows * nc * 2 <= slots && vectors > nc * SHORT) nc *= 2;
-  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, done, rows, nc, done > 0, st)
-                                          : launch_score<DT, 256, true>(a, done, rows, nc, done > 0, st);
+  return (vectors + nc - 1) / nc <= SHORT ? launch_score<DT, 256, false>(a, done, rows, nc, st)
+                                          : launch_score<DT, 256, true>(a, done, rows, nc, st);
 }
 
 }  // namespace
