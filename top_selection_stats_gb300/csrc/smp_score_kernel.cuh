@@ -41,16 +41,15 @@ constexpr int SSMALL = 16;    // and of 64
 constexpr int SFIRST = 64;    // values the first bound is taken from
 constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
 // Ring: chunks a warp has in flight.  Two where the stream of bytes is the bound (4093
-// x 128256 bf16 without alternatives 152 us, 157 with one; 2000 x 128256 f32 155
-// and 161); one where the row's other work is, 16-bit logits with a mask or with
-// alternatives: what the ring leaves is cache for the mask and for what is read
-// again (512 x 151936 masked with 8: 53.7 us, 56.4 with two; 2000 x 40000 with 5:
-// 50.8 and 54.6).
-constexpr int ring_stages(int dt, bool top, bool mask) { return dt != SMP_F32 && (top || mask) ? 1 : 2; }
+// x 128256 bf16 without alternatives 152 us, 157 with one; 4000 x 128256 masked 177 and
+// 180; 2000 x 128256 f32 155 and 161); one where the row's other work is, 16-bit logits
+// with alternatives: what the ring leaves is cache for what is read again (512 x 151936
+// masked with 8: 48.5 us, 51.3 with two; 2000 x 40000 with 5: 50.5 and 55.2).
+constexpr int ring_stages(int dt, bool top) { return dt != SMP_F32 && top ? 1 : 2; }
 constexpr int SMOST = 2;      // the larger of both
 // Legal values of a lane in a chunk (of 64 or 32) that are taken one by one from the
-// stage: 4000 x 128256 bf16, a third of the rows with one token in twenty legal,
-// 184 us, 191 with every chunk taken whole; 512 x 151936 with 8 alternatives 50.2 and 53.7.
+// stage: 912 x 151936 bf16 with 8 alternatives, a third of the rows with one token in
+// twenty legal, 72.2 us, 75.2 with every chunk taken whole; 512 rows 48.5 and 50.4.
 constexpr int SFEW = 12;
 constexpr float SLAG = 8.f;
 constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   constexpr int NW = CV * VE / 1024;        // mask words of a lane
   __shared__ __align__(16) Scratch<ST, LONG, TOP> sh;
   extern __shared__ __align__(128) uint8_t ring_raw[];
-  constexpr int SSTAGES = ring_stages(DT, TOP, MASK);
+  constexpr int SSTAGES = ring_stages(DT, TOP);
   using LI = Lists<ST, LONG>;
   static_assert(!LONG || sizeof(LI) <= (ST * 16 << SLNU) * SSTAGES, "the lists fit where the ring was");
   LI& li = *reinterpret_cast<LI*>(LONG ? ring_raw : sh.lists);
@@ -448,20 +447,6 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     float bmax = -INFINITY;
     for (int i = 0; i < chunks; ++i) {
       const int c = mine + i * (SW * CV), slot = i % SSTAGES;
-      uint32_t next[MASK ? NW : 1];
-      if constexpr (MASK) {
-        words += SW * CV * VE / 32;
-        words_left -= SW * CV * VE / 32;
-        if (i + 1 < chunks) load_bits(next, words, bit0 & 31, words_left);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], (i / SSTAGES) & 1, SWAIT))) {
-        // the copies behind it are given as long, then the warp goes on without
-        for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
-          mbar_wait_bounded(&full[k % SSTAGES], (k / SSTAGES) & 1, SWAIT);
-        bad = SC_LATE;
-        break;
-      }
-      float top = -INFINITY;
       int most = SFEW + 1;  // legal values of a lane, at most
       uint32_t lo = 0u, hi = 0u;
       bool whole = true;
@@ -471,7 +456,18 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
           lane_bits(lo, hi);
           most = __reduce_max_sync(0xffffffffu, __popc(lo) + __popc(hi));
         }
+        words += SW * CV * VE / 32;
+        words_left -= SW * CV * VE / 32;
+        if (i + 1 < chunks) load_bits(bits, words, bit0 & 31, words_left);
       }
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], (i / SSTAGES) & 1, SWAIT))) {
+        // the copies behind it are given as long, then the warp goes on without
+        for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
+          mbar_wait_bounded(&full[k % SSTAGES], (k / SSTAGES) & 1, SWAIT);
+        bad = SC_LATE;
+        break;
+      }
+      float top = -INFINITY;
       if (MASK && most <= SFEW) {  // few: taken one by one, straight from the stage
         const raw* stage = reinterpret_cast<const raw*>(ring + slot * CV + lane);
         const int first = (c + lane) * VE - lead;
@@ -517,10 +513,6 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
           sh.bucket[(i >> gshift) * ST + tid] = order32(bmax);
           bmax = -INFINITY;
         }
-      }
-      if constexpr (MASK) {  // here, not earlier: the copy waits for the load
-#pragma unroll
-        for (int w = 0; w < NW; ++w) bits[w] = next[w];
       }
     }
   } else if (chunks) {
@@ -646,15 +638,16 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
         if (p < SCAND) li.cand[p] = k;
       }
     };
-    // The vector's values at or above the bound.  Small code rather than
-    // unrolled: what runs once per row pays for its fetch.
-    auto offer_vector = [&](const uint4& y, int j0, bool masked) {
+    // The vector's legal values (a bit each) at or above the bound.  Small code rather
+    // than unrolled: what runs once per row pays for its fetch.
+    auto offer_vector = [&](const uint4& y, int j0, uint32_t which) {
       const float least = key_value(max(bound, (uint64_t)0x00800000u << 32));  // any finite value, at least
       float f[VE];
       sc_unpack<DT>(y, f);
       uint32_t hits = 0u;
 #pragma unroll
       for (int i = 0; i < VE; ++i) hits |= f[i] >= least ? 1u << i : 0u;
+      hits &= which;
       while (hits) {
         const int i = __ffs(hits) - 1, w = DT == SMP_F32 ? i : i >> 1;
         hits &= hits - 1;
@@ -662,7 +655,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
         raw value;
         if constexpr (DT == SMP_F32) value = __uint_as_float(word);
         else value = (raw)(i & 1 ? word >> 16 : word);
-        if (!masked || legal(j0 + i)) offer(TY::value(value), j0 + i);
+        offer(TY::value(value), j0 + i);
       }
     };
     if constexpr (LONG) {
@@ -696,7 +689,10 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
           if (v >= v1) continue;
         }
         const bool here = !LONG && i < SKEPT;
-        offer_vector(here ? li.kept[i] : src[v], v * VE - lead, !here);
+        const int j0 = v * VE - lead;
+        uint32_t which = ~0u;  // its mask is on the way together with it
+        if (MASK && !here) which = __funnelshift_r(bm[j0 >> 5], bm[(j0 + VE - 1) >> 5], j0 & 31);
+        offer_vector(here ? li.kept[i] : src[v], j0, which);
       }
       __syncthreads();
       found = sh.found;
@@ -781,7 +777,7 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
   cfg.blockDim = dim3(ST);
   cfg.stream = st;
   if (LONG) {
-    cfg.dynamicSmemBytes = (ST * 16 << SLNU) * ring_stages(DT, a.n > 0, a.bitmask != nullptr);
+    cfg.dynamicSmemBytes = (ST * 16 << SLNU) * ring_stages(DT, a.n > 0);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
         cudaSuccess)
       return SMP_ERR_CUDA;
