@@ -271,7 +271,9 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   // (8 x 128256: 4.3 to 4.0 us): nothing of a caller's is read or written before that
   // is complete.  It lets no other start early, whose CTAs would take their places
   // while these still have theirs, unevenly (256 x 128256 with 20 top: 26.6 us, not
-  // 21.6).  Of a call of two launches the second starts once all CTAs of the first have.
+  // 21.6).  Of a call of two or three launches the first starts after everything before
+  // it, and each later one once all CTAs of the one before it have started: all read only
+  // what was complete before the call, and their rows are their own.
   if (r0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (more) asm volatile("griddepcontrol.launch_dependents;");
   if (LONG) {
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     a.top_lp[(size_t)r * n + lane] =
         !sh.ok ? sc_nan() : k ? sc_logprob(key_value(k), sh.m, sh.log_mass, T) : -INFINITY;
   }
-  // the second launch ends only after the one it started beside
+  // a later launch ends only after the one it started beside, so the last ends last
   if (r0 && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -801,11 +803,12 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
 // 4000 x 5000 bf16 with 5 alternatives 27.6 us in CTAs of 4 warps, 33.0 of 8.
 // Rows up to four times as long as 8 warps' chunks are taken by 4 warps while they
 // fill the SMs (3000 x 16000 with 5: 38.7 us, 46.8 with 8), others by 8.  The rows left
-// when all others fill the SMs take a second launch, on what the first leaves
+// when all others fill the SMs take a launch of their own, on what the ones before leave
 // free, in clusters as large as still fit at once, while a warp has more than a
-// chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without the second
-// launch; 64 x 128256 bf16 with 20: 10.1 us in clusters of 4, 14.7 of 8 (two
-// rounds of CTAs).
+// chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without
+// it; 64 x 128256 bf16 with 20: 10.1 us in clusters of 4, 14.7 of 8 (two
+// rounds of CTAs).  So a call is one launch, two or, where rows of up to four times 8
+// warps' chunks leave at least a full round of CTAs of 8 warps, three.
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
