@@ -350,8 +350,8 @@ int smp_token_logprobs(const void* logits, smp_dtype dtype, int B, int V, int64_
  * d loss / d entropy[r] = grad_entropy[r]:
  *   grad[r][j] = (grad_logprobs[r] (1{j = target} - p_j)
  *                 - grad_entropy[r] p_j (log p_j + entropy[r])) / T,
- * computed in binary32 and rounded once to `dtype`; 0 for tokens that are not
- * legal.  grad_logprobs counts nothing in a row without a target or with one
+ * computed in binary32 and rounded once to `dtype` (a result past its range is an
+ * infinity); 0 for tokens that are not legal.  grad_logprobs counts nothing in a row without a target or with one
  * that is not legal.  A row whose stats are not finite (a row that failed in
  * the forward call), or whose temperature or target is invalid, gets zeros.
  *   logits, bitmask, temperature, targets: as given to the forward call.

@@ -4,7 +4,11 @@
 //     grad_j = p_j (a + b d_j) + [j = target] g / T,
 //     a = -(g + g_H (H - L)) / T,   b = -g_H ln 2 / T.
 // 2^d flushes results below 2^-126 to zero, which a small T would make
-// visible: p is taken times 2^24 and a, b times 2^-24.
+// visible: p is taken times 2^24 and a, b times 2^-24.  A row whose a, b or g / T leave
+// binary32's normal range all the same (T = 1e-40, gradients of 1e-32 or 1e38) takes
+// another power than 2^24, with which a and b stay inside it, and has its target's
+// value from the formula: only results that pass the range themselves become infinite,
+// and 0 probability gives 0, not 0 times infinity.
 //
 // One read and one write of the row: bound by HBM.  A row is cut into segments,
 // one per CTA; a thread has GU 16-byte vectors in flight.  A CTA reads the
@@ -71,7 +75,8 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
   const bool live = sc_temperature_ok(T) && t >= -1 && t < a.V && fabsf(m) < INFINITY && fabsf(L) < INFINITY;
   auto legal = [&](int j) { return !bm || ((bm[j >> 5] >> (j & 31)) & 1u); };
   // a target that is not legal has no gradient
-  if (!live || t < 0 || !legal(t) || !(TY::value(row[t]) > -INFINITY)) g = 0.f;
+  const float xt = live && t >= 0 && legal(t) ? TY::value(row[t]) : -INFINITY;
+  if (!(xt > -INFINITY)) g = 0.f;
   if (in_place) {  // every CTA of the row has read the target's logit before one writes
     cluster_arrive();
     cluster_wait();
@@ -85,6 +90,28 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
   q.at = g / T;
   q.t = g != 0.f ? t : -1;
   const bool zero = !live || (g == 0.f && gh == 0.f);
+  // with these the factors are in range (H - L is at most 17): no wait for the quotients
+  const float size = fmaxf(fabsf(g), fabsf(gh));
+  bool far = !zero && !(T > 0x1p-60f && T < 0x1p20f && size > 0x1p-70f && size < 0x1p60f);
+  float most;
+  if (far) {
+    most = fmaxf(fabsf(q.c0), fabsf(q.c1));
+    far = !(most >= 0x1p-126f && most < INFINITY && fabsf(q.at) < INFINITY);
+  }
+  if (far) {
+    // Small: p times 2^-24, factors that keep their bits.  Large (T < 1): p times 2^63,
+    // a and b up to 2^110, so that b d, with d down to SC_DMIN, stays finite; past 2^173
+    // they count as that.
+    const bool small = most < 0x1p-126f;
+    const float sg = small ? 0x1p24f : 0x1p-32f, st = small ? T : T * 0x1p31f;
+    const float gs = g * sg, hs = gh * sg;
+    auto factor = [&](float c) { return fabsf(c) > 0x1p110f ? copysignf(0x1p110f, c) : c; };
+    q.c0 = factor(-(gs + (a.g_ent ? hs * (H - L) : 0.f)) / st);
+    q.c1 = factor(-hs * SC_LN2 / st);
+    q.l2 = L / SC_LN2 + (small ? 24.f : -63.f);
+    const float lp = (xt - m) / T - L, p = expf(lp);
+    q.at = (gs - (p > 0.f ? p * (gs + (a.g_ent ? hs * (lp + H) : 0.f)) : 0.f)) / st * (small ? 0x1p-24f : 0x1p63f);
+  }
 
   // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(raw));
@@ -127,7 +154,8 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
         for (int i = 0; i < VE; i += 2) grad_pair<ENT>(q, f[i], f[i + 1]);
         if (q.t >= j0 && q.t < j0 + VE) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) f[i] += q.t == j0 + i ? q.at : 0.f;
+          for (int i = 0; i < VE; ++i)
+            if (q.t == j0 + i) f[i] = far ? q.at : f[i] + q.at;
         }
         __stcs(dst + v, sc_pack<DT>(f));
       } else {  // a row's ends, or a result whose rows start elsewhere in their vectors
@@ -137,7 +165,7 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
           if (!zero && legal(j)) {
             y = TY::value(row[j]);
             grad_pair<ENT>(q, y, other);
-            if (j == q.t) y += q.at;
+            if (j == q.t) y = far ? q.at : y + q.at;
           }
           out[j] = TY::store(y);
         }
