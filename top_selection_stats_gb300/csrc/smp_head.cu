@@ -473,8 +473,7 @@ EncodeTiled encoder() {
   static const EncodeTiled fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
+    if (!sc_ok(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q)) ||
         q != cudaDriverEntryPointSuccess)
       p = nullptr;
     return reinterpret_cast<EncodeTiled>(p);
@@ -509,8 +508,7 @@ int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* cta
   // binary32 accumulators, both operands of `type` and K-major, N = BN, M = BM
   const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(BN >> 3) << 17) |
                          ((uint32_t)(SH::BM >> 4) << 24);
-  if (cudaFuncSetAttribute(head_kernel<BN, PAIR, AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) !=
-      cudaSuccess)
+  if (!sc_ok(cudaFuncSetAttribute(head_kernel<BN, PAIR, AR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM)))
     return SMP_ERR_CUDA;
   constexpr int each = PAIR ? 2 : 1;
   const long long tiles = (long long)((a.N + SH::BM - 1) / SH::BM) * ((a.V + BN - 1) / BN);
@@ -530,7 +528,7 @@ int launch_head(const HeadArgs& a, int dtype, int sms, cudaStream_t st, int* cta
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR, AR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)) == cudaSuccess
+  return sc_ok(cudaLaunchKernelEx(&cfg, head_kernel<BN, PAIR, AR>, a, mh, mw, idesc, (uint32_t)(rows * HBK * 2)))
              ? SMP_OK : SMP_ERR_CUDA;
 }
 
@@ -557,7 +555,7 @@ int head_enqueue(const HeadArgs& a, int dtype, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, head_join, a, 2 * tiles_of(a.N, a.V), ctas) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  return sc_ok(cudaLaunchKernelEx(&cfg, head_join, a, 2 * tiles_of(a.N, a.V), ctas)) ? SMP_OK : SMP_ERR_CUDA;
 }
 
 }  // namespace smp

@@ -239,11 +239,17 @@ struct HeadArgs {
   int N, V, D;
 };
 
+// Whether a runtime call succeeded.  An error is taken off the thread's last error: it is
+// reported by this call's status, and a later launch's check must not find it.
+inline bool sc_ok(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess;
+}
+
 // SMs of the current device; 0 when it cannot be asked.
 inline int sc_sm_count() {
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (!sc_ok(cudaGetDevice(&dev)) || !sc_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return 0;
   return sms;
 }

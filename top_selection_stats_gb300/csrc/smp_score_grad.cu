@@ -205,7 +205,7 @@ int launch_grad(const GradArgs& a, int sms, cudaStream_t st) {
   cfg.numAttrs = in_place ? 2 : 1;
   const cudaError_t e = a.g_ent ? cudaLaunchKernelEx(&cfg, grad_kernel<DT, true>, a, nc, seg, in_place)
                                 : cudaLaunchKernelEx(&cfg, grad_kernel<DT, false>, a, nc, seg, in_place);
-  return e == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  return sc_ok(e) ? SMP_OK : SMP_ERR_CUDA;
 }
 
 }  // namespace

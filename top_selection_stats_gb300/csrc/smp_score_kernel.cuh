@@ -780,8 +780,7 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
   cfg.stream = st;
   if (LONG) {
     cfg.dynamicSmemBytes = (ST * 16 << SLNU) * ring_stages(DT, a.n > 0);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
-        cudaSuccess)
+    if (!sc_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes)))
       return SMP_ERR_CUDA;
   }
   cudaLaunchAttribute attr[2];
@@ -796,7 +795,7 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, more) == cudaSuccess ? SMP_OK : SMP_ERR_CUDA;
+  return sc_ok(cudaLaunchKernelEx(&cfg, kernel, a, nc, seg, gshift, r0, more)) ? SMP_OK : SMP_ERR_CUDA;
 }
 
 // Short rows, one chunk a warp, take CTAs of 2 or 4 warps, so that an SM holds many:
