@@ -5,7 +5,7 @@ states (the handle-free calls of include/smp.h).  Argument marshalling only.
 Every tensor lives on the logits' (the hidden states') CUDA device and is
 contiguous; the calls run on that device's current stream.  ``out`` takes what
 an earlier call of the same shape returned and writes it again, so a serving
-loop allocates nothing.
+loop allocates nothing (head_logprobs: with ``workspace`` as well).
 """
 import torch
 
@@ -142,20 +142,14 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
     return out
 
 
-class _HeadResults(dict):
-    """head_logprobs' results, with the workspace of their call for the next one that gets
-    them as ``out``."""
-    __slots__ = ("workspace",)
-
-
 def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, workspace=None,
                   lib=None):
     """smp_head_logprobs: token_logprobs' logprobs, entropy, stats and status
     for logits = hidden @ weight.T (hidden [N, D], weight [V, D], both bfloat16
     or both float16, row lengths a multiple of 8; with ``D`` only the first D
     columns count), without the logits in memory.  workspace: uint8, at least
-    head_workspace(N, V) bytes; when None, that of the call that made ``out``, or a
-    new one."""
+    head_workspace(N, V) bytes, the call's own until its work on the stream is done; when
+    None, one is allocated for the call and given back to the stream's allocator."""
     L = lib or load_library()
     N, ldh = _matrix(hidden, "hidden", (torch.bfloat16, torch.float16))
     V, ldw = _matrix(weight, "weight", (torch.bfloat16, torch.float16))
@@ -173,17 +167,13 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
     tg = _need(targets, "targets", dev, _I32, N)
     tp = _opt(temperature, "temperature", dev, _F32, N)
     if out is None:
-        out = _HeadResults(logprobs=torch.empty(N, dtype=_F32, device=hidden.device),
-                           entropy=torch.empty(N, dtype=_F32, device=hidden.device),
-                           stats=torch.empty((N, 2), dtype=_F32, device=hidden.device),
-                           status=torch.empty(N, dtype=_I32, device=hidden.device))
+        out = dict(logprobs=torch.empty(N, dtype=_F32, device=hidden.device),
+                   entropy=torch.empty(N, dtype=_F32, device=hidden.device),
+                   stats=torch.empty((N, 2), dtype=_F32, device=hidden.device),
+                   status=torch.empty(N, dtype=_I32, device=hidden.device))
     nbytes = L.smp_head_workspace(N, V)
     if workspace is None:
-        workspace = getattr(out, "workspace", None)
-        if workspace is None or workspace.numel() < nbytes or workspace.get_device() != dev:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
-            if isinstance(out, _HeadResults):
-                out.workspace = workspace
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
     elif (workspace.dtype != torch.uint8 or workspace.get_device() != dev
           or not workspace.is_contiguous() or workspace.numel() < nbytes):
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {nbytes} bytes on cuda:{dev}")
