@@ -63,7 +63,7 @@ struct HeadShape {
 // more evenly over the SMs.  More states: two CTAs on a tile of 256 x 256, so
 // that each stages half of the weights.
 int tile_tokens(int N) { return N <= HBM ? 128 : 256; }
-int tiles_of(int N, int V) { return (V + tile_tokens(N) - 1) / tile_tokens(N); }
+int tiles_of(int N, int V) { return (V - 1) / tile_tokens(N) + 1; }  // V >= 1, up to the largest int
 
 struct HeadBars {
   uint64_t full[10], empty[10], acc_full[4], acc_empty[4], drain;
