@@ -250,11 +250,13 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   uint32_t bits[MASK ? NW : 1];
   uint4* ring = reinterpret_cast<uint4*>(ring_raw) + warp * (SSTAGES * CV);
   uint64_t* full = sh.full + (LONG ? warp * SSTAGES : 0);
-  auto fetch = [&](int i) {  // chunk i into its stage; what it does not fill holds nothing
+  // Chunk i into its stage; what it does not fill holds nothing, written by the lane that
+  // reads it (only votes lie between the two, which order no memory of other lanes).
+  auto fetch = [&](int i) {
     if (i >= chunks) return;
     const int c = mine + i * (SW * CV), k = min(CV, v1 - c);
     uint4* stage = ring + (i % SSTAGES) * CV;
-    for (int e = k + lane; e < CV; e += 32) stage[e] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
+    for (int e = k + ((lane - k) & 31); e < CV; e += 32) stage[e] = make_uint4(WD::NONE, WD::NONE, WD::NONE, WD::NONE);
     if (lane == 0) {
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(&full[i % SSTAGES], k * 16);
