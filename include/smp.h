@@ -310,7 +310,7 @@ int smp_gumbel_sample(smp_handle h, const void* logits, smp_dtype dtype, int B, 
  * failed to sample).  Row status: SMP_ERR_INVALID_PARAM (bad temperature, a
  * target outside [-1, V)), SMP_ERR_NONFINITE (NaN or +inf in a legal slot),
  * SMP_ERR_EMPTY (no legal token), SMP_ERR_TIMEOUT (a bounded device wait, about
- * two seconds, ran out).  Rows may start at any address that their type
+ * two seconds unless set otherwise, ran out).  Rows may start at any address that their type
  * allows; unaligned ones are as fast.  Sums are in binary32 (typical errors: a
  * few 1e-7 of a result).  The same call gives the same bits each time; the last
  * bits of a row's sums may depend on its alignment and on how many rows
@@ -391,6 +391,12 @@ int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
 /* Bytes of workspace that smp_head_logprobs needs for N rows and V tokens (0
  * for N or V < 1). */
 int64_t smp_head_workspace(int N, int V);
+
+/* Bounds the device-side waits of smp_token_logprobs calls made from now on, by
+ * any thread, to `cycles` SM clock cycles (<= 0: the default, 4e9, about two
+ * seconds; a captured graph keeps the bound it was captured with).  A wait
+ * that runs out gives SMP_ERR_TIMEOUT for its row.  Always SMP_OK. */
+int smp_set_scoring_wait_limit(long long cycles);
 
 /* Optional per-row diagnostics for subsequent calls on this handle: when
  * row_info is not NULL, each call writes int32 [B][4] to it (DEVICE memory

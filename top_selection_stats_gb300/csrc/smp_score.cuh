@@ -26,6 +26,9 @@ constexpr float SC_LN2 = 0.6931471805599453f;
 constexpr float SC_DMIN = -1.0e4f;
 constexpr int SC_MAX_V = 1 << 24;
 constexpr int SC_MAX_TOP = 32;
+// SM cycles that a wait may take, unless a call is given fewer (about two seconds); what is
+// in flight when one runs out is always given as long as this to land.
+constexpr long long SC_WAIT = 4000000000ll;
 
 __device__ __forceinline__ float sc_nan() { return __int_as_float(0x7fffffff); }
 
@@ -207,6 +210,30 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A wait for a barrier's phase (shared memory address `bar`), `limit` SM cycles at most
+// from a first look that does not park the thread: with a limit of 1 every wait that would
+// wait fails.
+__device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, long long limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  const long long t0 = ok ? 0 : clock64();
+  while (!ok) {
+    if (clock64() - t0 > limit) return false;
+    asm volatile(  // parked up to a microsecond
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+  }
+  return true;
+}
+
 struct ScoreArgs {
   const void* logits;
   long long ld;
@@ -217,6 +244,7 @@ struct ScoreArgs {
   int32_t *rank, *status, *top_ids;
   float* top_lp;
   int B, V, W, n;
+  long long wait_limit;
 };
 struct GradArgs {
   const void* logits;

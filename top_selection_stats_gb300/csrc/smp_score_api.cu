@@ -1,5 +1,7 @@
 // smp_score_api.cu -- argument checks of the scoring calls declared in
-// include/smp.h.  Nothing here allocates, synchronises or throws.
+// include/smp.h, and the bound on their waits.  Nothing here allocates,
+// synchronises or throws.
+#include <atomic>
 #include <cstdint>
 
 #include "smp_score.cuh"
@@ -10,6 +12,7 @@ namespace {
 bool dtype_ok(int dt) { return dt == SMP_F32 || dt == SMP_BF16 || dt == SMP_F16; }
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 constexpr int HEAD_MAX = 1 << 20;
+std::atomic<long long> g_wait_limit{SC_WAIT};
 }  // namespace
 
 extern "C" {
@@ -41,6 +44,7 @@ int smp_token_logprobs(const void* logits, smp_dtype dtype, int B, int V, int64_
   a.V = V;
   a.W = (V + 31) / 32;
   a.n = n;
+  a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   cudaStream_t st = (cudaStream_t)stream;
   return dtype == SMP_F32 ? score_f32(a, st) : dtype == SMP_BF16 ? score_bf16(a, st) : score_f16(a, st);
 }
@@ -107,6 +111,11 @@ int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
   a.V = V;
   a.D = D;
   return head_enqueue(a, (int)dtype, (cudaStream_t)stream);
+}
+
+int smp_set_scoring_wait_limit(long long cycles) {
+  g_wait_limit.store(cycles > 0 ? cycles : SC_WAIT, std::memory_order_relaxed);
+  return SMP_OK;
 }
 
 int64_t smp_head_workspace(int N, int V) { return N < 1 || V < 1 ? 0 : head_workspace(N, V); }

@@ -52,7 +52,6 @@ constexpr int SMOST = 2;      // the larger of both
 // twenty legal, 72.2 us, 75.2 with every chunk taken whole; 512 rows 48.5 and 50.4.
 constexpr int SFEW = 12;
 constexpr float SLAG = 8.f;
-constexpr long long SWAIT = 4000000000ll;  // SM cycles a copy is waited for: about two seconds
 
 // Order key of a value: larger = earlier; 0 = none (not legal).
 __device__ __forceinline__ uint32_t order32(float x) {
@@ -464,10 +463,11 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
         words_left -= SW * CV * VE / 32;
         if (i + 1 < chunks) load_bits(bits, words, bit0 & 31, words_left);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], (i / SSTAGES) & 1, SWAIT))) {
-        // the copies behind it are given as long, then the warp goes on without
-        for (int k = i + 1; k < min(chunks, i + SSTAGES); ++k)
-          mbar_wait_bounded(&full[k % SSTAGES], (k / SSTAGES) & 1, SWAIT);
+      if (!__all_sync(0xffffffffu, sc_wait(smem_u32(&full[slot]), (i / SSTAGES) & 1, a.wait_limit))) {
+        // no copy is left in flight, into what is used for other things next; then the warp
+        // goes on without the rest of its chunks
+        for (int k = i; k < min(chunks, i + SSTAGES); ++k)
+          sc_wait(smem_u32(&full[k % SSTAGES]), (k / SSTAGES) & 1, SC_WAIT);
         bad = SC_LATE;
         break;
       }
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       for (int i = 0; i < SFIRST; ++i) above += firsts[i] > v || (firsts[i] == v && i < tid);
       if (above == n - 1) sh.low = max(v, 1u);  // 0: fewer than n; any legal value
     }
-    __syncthreads();
+    const bool late = __syncthreads_or(bad & SC_LATE);  // the row fails: not all buckets are there, nothing to search
     const uint32_t low = sh.low;
     uint64_t bound = (uint64_t)low << 32;
     auto offer = [&](float y, int j) {
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       }
     };
     if constexpr (LONG) {
-      const int buckets = (chunks + (1 << gshift) - 1) >> gshift;
+      const int buckets = late ? 0 : (chunks + (1 << gshift) - 1) >> gshift;
       for (int b = 0; b < buckets; ++b)
         if (sh.bucket[b * ST + tid] >= low) li.queue[atomicAdd(&sh.queued, 1)] = (unsigned short)(b * ST + tid);
     } else if (order32(mx) >= low) {

@@ -191,3 +191,9 @@ def head_logprobs(hidden, weight, targets, temperature=None, D=None, out=None, w
 def head_workspace(N, V, lib=None):
     """smp_head_workspace: bytes of workspace that head_logprobs needs."""
     return (lib or load_library()).smp_head_workspace(N, V)
+
+
+def set_scoring_wait_limit(cycles=0, lib=None):
+    """smp_set_scoring_wait_limit: bound on each device wait of later token_logprobs calls of
+    the process (SM cycles; 0 = default)."""
+    _check((lib or load_library()).smp_set_scoring_wait_limit(int(cycles)), "smp_set_scoring_wait_limit")
