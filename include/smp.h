@@ -392,10 +392,11 @@ int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
  * for N or V < 1). */
 int64_t smp_head_workspace(int N, int V);
 
-/* Bounds the device-side waits of smp_token_logprobs calls made from now on, by
- * any thread, to `cycles` SM clock cycles (<= 0: the default, 4e9, about two
- * seconds; a captured graph keeps the bound it was captured with).  A wait
- * that runs out gives SMP_ERR_TIMEOUT for its row.  Always SMP_OK. */
+/* Bounds the device-side waits of smp_token_logprobs and smp_head_logprobs calls
+ * made from now on, by any thread, to `cycles` SM clock cycles (<= 0: the
+ * default, 4e9, about two seconds; a captured graph keeps the bound it was
+ * captured with).  A wait that runs out gives SMP_ERR_TIMEOUT for its row, in
+ * smp_head_logprobs for all rows of the call.  Always SMP_OK. */
 int smp_set_scoring_wait_limit(long long cycles);
 
 /* Optional per-row diagnostics for subsequent calls on this handle: when

@@ -28,8 +28,8 @@
 // each call.
 //
 // Every wait on a barrier is bounded.  One that expires makes all roles of the
-// CTA leave; copies and products in flight are waited for, tensor memory is
-// freed, and all rows of the call return SMP_ERR_TIMEOUT.
+// CTA, in a pair of both CTAs, leave; copies and products in flight are waited for
+// (settle), tensor memory is freed, and all rows of the call return SMP_ERR_TIMEOUT.
 #include <cuda.h>
 
 #include "smp_score.cuh"
@@ -43,7 +43,6 @@ constexpr int HSEG = 8;                // stages that one accumulator sums
 constexpr int HEPI = 8;                // epilogue warps: two groups of four
 constexpr int HTHREADS = (HEPI + 2) * 32;
 constexpr int HFLAGS = 1024;           // workspace: one word per CTA, then the tiles' states
-constexpr long long HWAIT = 4000000000ll;  // SM cycles: about two seconds
 
 // AR: rows of states that a stage has room for.  With AR < 128 the products read on into
 // the weights behind them: rows of the tile that no state has.
@@ -68,6 +67,7 @@ int tiles_of(int N, int V) { return (V - 1) / tile_tokens(N) + 1; }  // V >= 1, 
 struct HeadBars {
   uint64_t full[10], empty[10], acc_full[4], acc_empty[4], drain;
   uint32_t tmem;
+  uint32_t issued[2];  // first CTA: stages that each CTA of the pair has sent copies for
   int fail;
 };
 
@@ -84,41 +84,38 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(b)), "r"(parity), "r"(1000u)
-      : "memory");
-  return ok != 0u;
+// Takes bytes that no copy will bring off what the phase still expects.
+__device__ __forceinline__ void bar_deduct(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes)
+               : "memory");
 }
-// Waits for the phase; false when it does not come within `HWAIT` cycles or
-// another role has given up.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* fail) {
-  if (bar_try(b, parity)) return true;
+// The address of `p` in the pair's CTA of this rank; the first's.
+__device__ __forceinline__ uint32_t pair_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t first_addr(const void* p) { return pair_addr(p, 0); }
+__device__ __forceinline__ void pair_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Waits for the phase; false when it does not come within `limit` cycles of a first look,
+// which makes all roles leave, in a pair the other CTA's as well, or when another has
+// given up.  Every look parks: one that does not, before these, cost the thread that
+// issues the products 1 to 4 % of the call (4096 x 128256 x 4096: 2435 to 2539 us).
+template <bool PAIR>
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, int* fail, long long limit) {
+  if (sc_park(smem_addr(b), parity)) return true;
   const long long t0 = clock64();
-  while (!bar_try(b, parity)) {
-    if (*fail) return false;
-    if (clock64() - t0 > HWAIT) {
-      *fail = 1;
+  while (!sc_park(smem_addr(b), parity)) {
+    if (*(volatile int*)fail) return false;
+    if (clock64() - t0 > limit) {
+      *(volatile int*)fail = 1;
+      if constexpr (PAIR) pair_store(pair_addr(fail, (blockIdx.x & 1) ^ 1), 1u);
       return false;
     }
   }
   return true;
-}
-// The same without a look at the flag: for what is in flight when a role leaves.
-__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!bar_try(b, parity) && clock64() - t0 <= HWAIT) {
-  }
-}
-// The address of the pair's first CTA's `p`.
-__device__ __forceinline__ uint32_t first_addr(const void* p) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
-  return r;
 }
 __device__ __forceinline__ void bar_arrive_first(uint64_t* b) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_addr(b)) : "memory");
@@ -175,6 +172,21 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+// Copies in flight when the roles have left: waits until the last phase of each stage of
+// the first CTA is complete, which counts both CTAs' copies.  Where only one of the two
+// got as far, the phase is made to expect that one's bytes: neither can be a whole
+// ring ahead, as a stage is filled again only after products that had both halves.
+template <bool PAIR, int STAGES>
+__device__ __noinline__ void settle(HeadBars* bars, uint32_t bytes) {
+  auto uses = [](uint32_t n, uint32_t st) { return n > st ? (n - st - 1) / STAGES + 1 : 0u; };
+  for (uint32_t st = 0; st < STAGES; ++st) {
+    const uint32_t u0 = uses(bars->issued[0], st), u1 = PAIR ? uses(bars->issued[1], st) : u0;
+    if (u0 > u1) bar_deduct(&bars->full[st], bytes);
+    if (u1 > u0) bar_expect(&bars->full[st], bytes);
+    if (u0 | u1) sc_wait(smem_addr(&bars->full[st]), (max(u0, u1) - 1) & 1, SC_WAIT);
+  }
+}
+
 // 32 columns of this thread's row (the warp's 32 lanes of tensor memory).
 __device__ __forceinline__ void acc_load(uint32_t addr, float (&v)[32]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -206,7 +218,9 @@ __global__ void __launch_bounds__(HTHREADS, 1)
   const int mt = (a.N + SH::BM - 1) / SH::BM, vt = (a.V + BN - 1) / BN;
   const int kt = (a.D + HBK - 1) / HBK;
   const long long tiles = (long long)mt * vt;
-  volatile int* fail = &bars.fail;
+  int* fail = &bars.fail;
+  volatile int* failed = fail;
+  const long long limit = a.wait_limit;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < SH::STAGES; ++i) {
@@ -251,11 +265,11 @@ __global__ void __launch_bounds__(HTHREADS, 1)
   if (warp == HEPI) {  // copies
     if (lane == 0) {
       uint32_t i = 0;
-      for (long long tile = first; tile < tiles && !*fail; tile += stride) {
+      for (long long tile = first; tile < tiles && !*failed; tile += stride) {
         const int m0 = (int)(tile % mt) * SH::BM + peer * HBM, v0 = (int)(tile / mt) * BN + peer * SH::B_ROWS;
         for (int k = 0; k < kt; ++k, ++i) {
           const uint32_t st = i % SH::STAGES, use = i / SH::STAGES;
-          if (use && !bar_wait(&bars.empty[st], (use - 1) & 1, fail)) break;
+          if (use && !bar_wait<PAIR>(&bars.empty[st], (use - 1) & 1, fail, limit)) break;
           uint8_t* dst = ring + st * (SH::A_BYTES + SH::B_BYTES);
           if (!peer) bar_expect(&bars.full[st], (a_bytes + SH::B_BYTES) * (PAIR ? 2 : 1));
           const uint32_t bar = PAIR ? first_addr(&bars.full[st]) : smem_addr(&bars.full[st]);
@@ -264,26 +278,24 @@ __global__ void __launch_bounds__(HTHREADS, 1)
         }
       }
       asm volatile("griddepcontrol.launch_dependents;");  // head_join may get ready
-      // the last use of each stage: its products are done, or, when a wait ran
-      // out, its copies have at least landed, before the CTA ends (a pair's count on the
-      // first CTA's barriers, and neither ends before the other)
-      for (uint32_t j = i > SH::STAGES ? i - SH::STAGES : 0; j < i; ++j) {
-        const bool done = !*fail && bar_wait(&bars.empty[j % SH::STAGES], (j / SH::STAGES) & 1, fail);
-        if (!done && !peer) bar_drain(&bars.full[j % SH::STAGES], (j / SH::STAGES) & 1);
-      }
+      if (PAIR && peer) pair_store(first_addr(&bars.issued[1]), i);
+      else bars.issued[0] = i;
+      // the last use of each stage: its products are done before the CTA ends
+      for (uint32_t j = i > SH::STAGES ? i - SH::STAGES : 0; j < i; ++j)
+        if (!bar_wait<PAIR>(&bars.empty[j % SH::STAGES], (j / SH::STAGES) & 1, fail, limit)) break;
     }
   } else if (warp == HEPI + 1) {  // products
     if (lane == 0 && !peer) {
       uint32_t i = 0, sg = 0;
-      for (long long tile = first; tile < tiles && !*fail; tile += stride) {
-        for (int k0 = 0; k0 < kt && !*fail; k0 += HSEG, ++sg) {
+      for (long long tile = first; tile < tiles && !*failed; tile += stride) {
+        for (int k0 = 0; k0 < kt && !*failed; k0 += HSEG, ++sg) {
           const uint32_t b = sg % SH::ACCS, use = sg / SH::ACCS;
-          if (use && !bar_wait(&bars.acc_empty[b], (use - 1) & 1, fail)) break;
+          if (use && !bar_wait<PAIR>(&bars.acc_empty[b], (use - 1) & 1, fail, limit)) break;
           fence_after();
           const int k1 = min(kt, k0 + HSEG);
           for (int k = k0; k < k1; ++k, ++i) {
             const uint32_t st = i % SH::STAGES;
-            if (!bar_wait(&bars.full[st], (i / SH::STAGES) & 1, fail)) break;
+            if (!bar_wait<PAIR>(&bars.full[st], (i / SH::STAGES) & 1, fail, limit)) break;
             fence_after();
             const uint32_t base = smem_addr(ring + st * (SH::A_BYTES + SH::B_BYTES));
             const uint64_t da = operand_desc(base), db = operand_desc(base + SH::A_BYTES);
@@ -292,12 +304,8 @@ __global__ void __launch_bounds__(HTHREADS, 1)
               mma<PAIR>(tmem + b * BN, da + 2 * q, db + 2 * q, idesc, k > k0 || q > 0);
             mma_commit<PAIR>(&bars.empty[st]);
           }
-          if (!*fail) mma_commit<PAIR>(&bars.acc_full[b]);
+          if (!*failed) mma_commit<PAIR>(&bars.acc_full[b]);
         }
-      }
-      if (*fail) {
-        mma_commit<PAIR>(&bars.drain);
-        bar_drain(&bars.drain, 0);
       }
     }
   } else {  // epilogue: group warp / 4 has half of the tile's columns
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(HTHREADS, 1)
       for (int k = 0; k < kt; k += HSEG, ++sg) {
         const uint32_t b = sg % SH::ACCS;
         // the warp leaves or stays as one: the loads below are the whole warp's
-        gone = !__all_sync(0xffffffffu, bar_wait(&bars.acc_full[b], (sg / SH::ACCS) & 1, fail));
+        gone = !__all_sync(0xffffffffu, bar_wait<PAIR>(&bars.acc_full[b], (sg / SH::ACCS) & 1, fail, limit));
         if (gone) break;
         fence_after();
         const uint32_t acc = tmem + b * BN + c0 + ((uint32_t)(warp & 3) * 32u << 16);
@@ -398,6 +406,19 @@ __global__ void __launch_bounds__(HTHREADS, 1)
   if constexpr (PAIR) {  // neither CTA's memory is used by the other any more
     cluster_arrive();
     cluster_wait();
+  }
+  if (*failed) {  // in a pair both CTAs see it, or neither: all roles have left
+    if (lane == 0 && warp == HEPI + 1) {
+      if (!peer) mma_commit<PAIR>(&bars.drain);  // by the thread that issued the products
+      sc_wait(smem_addr(&bars.drain), 0, SC_WAIT);
+    }
+    if (lane == 0 && warp == HEPI && !peer) settle<PAIR, SH::STAGES>(&bars, a_bytes + SH::B_BYTES);
+    __syncwarp();
+    __syncthreads();
+    if constexpr (PAIR) {
+      cluster_arrive();
+      cluster_wait();
+    }
   }
   if (warp == HEPI + 1) {
     fence_after();

@@ -210,10 +210,8 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A wait for a barrier's phase (shared memory address `bar`), `limit` SM cycles at most
-// from a first look that does not park the thread: with a limit of 1 every wait that would
-// wait fails.
-__device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, long long limit) {
+// Whether a barrier's phase is complete (shared memory address `bar`).
+__device__ __forceinline__ bool sc_done(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
@@ -221,16 +219,27 @@ __device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, long long
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
-  const long long t0 = ok ? 0 : clock64();
-  while (!ok) {
+  return ok != 0u;
+}
+// The same after a while: the thread is parked for up to a microsecond.
+__device__ __forceinline__ bool sc_park(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0u;
+}
+// A wait for a phase, `limit` SM cycles at most from a first look that does not park: with a
+// limit of 1 every wait that would wait fails.
+__device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, long long limit) {
+  if (sc_done(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
     if (clock64() - t0 > limit) return false;
-    asm volatile(  // parked up to a microsecond
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(1000u)
-        : "memory");
-  }
+  } while (!sc_park(bar, parity));
   return true;
 }
 
@@ -265,6 +274,7 @@ struct HeadArgs {
   int32_t* status;
   float4* part;  // workspace
   int N, V, D;
+  long long wait_limit;
 };
 
 // Whether a runtime call succeeded.  An error is taken off the thread's last error: it is

@@ -110,6 +110,7 @@ int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
   a.N = N;
   a.V = V;
   a.D = D;
+  a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   return head_enqueue(a, (int)dtype, (cudaStream_t)stream);
 }
 
