@@ -29,8 +29,8 @@
  * kept set, for comparison) and smp_spec_verify (speculative-decoding
  * verification against the kept sets' probabilities); smp_token_logprobs,
  * smp_token_logprobs_grad and smp_head_logprobs (scoring of given tokens, for
- * training on them or reporting them); smp_set_kernel
- * chooses between the two sampler kernels and smp_set_wait_limit bounds the
+ * training on them or reporting them); smp_set_kernel chooses between the two
+ * sampler kernels; smp_set_wait_limit and smp_set_scoring_wait_limit bound the
  * device-side waits.
  *
  * Conventions for every call:
@@ -310,11 +310,14 @@ int smp_gumbel_sample(smp_handle h, const void* logits, smp_dtype dtype, int B, 
  * failed to sample).  Row status: SMP_ERR_INVALID_PARAM (bad temperature, a
  * target outside [-1, V)), SMP_ERR_NONFINITE (NaN or +inf in a legal slot),
  * SMP_ERR_EMPTY (no legal token), SMP_ERR_TIMEOUT (a bounded device wait, about
- * two seconds unless set otherwise, ran out).  Rows may start at any address that their type
- * allows; unaligned ones are as fast.  Sums are in binary32 (typical errors: a
- * few 1e-7 of a result).  The same call gives the same bits each time; the last
- * bits of a row's sums may depend on its alignment and on how many rows
- * share the call.  Ids, ranks and statuses are exact. */
+ * two seconds unless set otherwise, ran out).  Rows of logits may start at any
+ * address that their type allows; unaligned ones are as fast, but the gradient's
+ * rows have to start as far into 16 bytes as the logits' (in place, or with the
+ * same address and row length modulo 16 bytes): otherwise it takes 2 (binary32)
+ * to 4 times as long (16 bits).  Sums are in binary32 (typical errors: a few 1e-7
+ * of a result).  The same call gives the same bits each time; the last bits of a
+ * row's sums may depend on its alignment and on how many rows share the call.
+ * Ids, ranks and statuses are exact. */
 
 /* Log-probabilities of given tokens, with entropy, rank and the n most likely
  * alternatives ("Sampling system design" post, section on logprobs: an API
@@ -350,10 +353,11 @@ int smp_token_logprobs(const void* logits, smp_dtype dtype, int B, int V, int64_
  * d loss / d entropy[r] = grad_entropy[r]:
  *   grad[r][j] = (grad_logprobs[r] (1{j = target} - p_j)
  *                 - grad_entropy[r] p_j (log p_j + entropy[r])) / T,
- * computed in binary32 and rounded once to `dtype` (a result past its range is an
- * infinity); 0 for tokens that are not legal.  grad_logprobs counts nothing in a row without a target or with one
- * that is not legal.  A row whose stats are not finite (a row that failed in
- * the forward call), or whose temperature or target is invalid, gets zeros.
+ * computed in binary32 and rounded once to `dtype` (a result past its range is
+ * an infinity); 0 for tokens that are not legal.  grad_logprobs counts nothing
+ * in a row without a target or with one that is not legal.  A row whose stats
+ * are not finite (a row that failed in the forward call), or whose temperature
+ * or target is invalid, gets zeros.
  *   logits, bitmask, temperature, targets: as given to the forward call.
  *   stats         : float [B][2], the forward call's.
  *   entropy       : float [B], the forward call's; needed with grad_entropy.

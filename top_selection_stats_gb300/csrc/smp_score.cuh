@@ -1,5 +1,5 @@
-// smp_score.cuh -- what the scoring kernels (smp_score.cu, smp_score_grad.cu,
-// smp_head.cu) share: the softmax state of a set of values, its merge, and
+// smp_score.cuh -- what the scoring kernels (smp_score_kernel.cuh,
+// smp_score_grad.cu, smp_head.cu) share: the softmax state of a set of values, its merge, and
 // the results computed from it.
 //
 // A set A of values x with largest m, scaled by s = log2(e) / T, is held as

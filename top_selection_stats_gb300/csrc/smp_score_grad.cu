@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
 
 // A CTA takes up to GSTEPS steps of GT * GU vectors of its row, fewer while that
 // leaves the SMs short of CTAs.  4096 x 128256 bf16: 297 us with 4 steps of 2
-// vectors a thread, 354 with 1, 327 with one step of 4 vectors; 1 x 128256: 2.2
-// us with 1 step, 3.6 with 4.  In place a row is one cluster, so at most GMAXC
+// vectors a thread, 354 with 1, 327 with one step of 4 vectors; 1 x 128256: 1.9
+// us with 1 step, 3.5 with 4.  In place a row is one cluster, so at most GMAXC
 // CTAs.
 template <int DT>
 int launch_grad(const GradArgs& a, int sms, cudaStream_t st) {

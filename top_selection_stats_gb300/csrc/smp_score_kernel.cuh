@@ -41,10 +41,10 @@ constexpr int SSMALL = 16;    // and of 64
 constexpr int SFIRST = 64;    // values the first bound is taken from
 constexpr int SLNU = 3;       // long segments: log2 of a lane's vectors in a chunk
 // Ring: chunks a warp has in flight.  Two where the stream of bytes is the bound (4093
-// x 128256 bf16 without alternatives 152 us, 157 with one; 4000 x 128256 masked 177 and
-// 180; 2000 x 128256 f32 155 and 161); one where the row's other work is, 16-bit logits
+// x 128256 bf16 without alternatives 152 us, 158 with one; 4000 x 128256 masked 178 and
+// 185; 2000 x 128256 f32 155 and 161); one where the row's other work is, 16-bit logits
 // with alternatives: what the ring leaves is cache for what is read again (512 x 151936
-// masked with 8: 48.5 us, 51.3 with two; 2000 x 40000 with 5: 50.5 and 55.2).
+// masked with 8: 48.3 us, 50.4 with two; 2000 x 40000 with 5: 51.1 and 53.8).
 constexpr int ring_stages(int dt, bool top) { return dt != SMP_F32 && top ? 1 : 2; }
 constexpr int SMOST = 2;      // the larger of both
 // Legal values of a lane in a chunk (of 64 or 32) that are taken one by one from the
@@ -801,9 +801,9 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
 }
 
 // Short rows, one chunk a warp, take CTAs of 2 or 4 warps, so that an SM holds many:
-// 4000 x 5000 bf16 with 5 alternatives 27.6 us in CTAs of 4 warps, 33.0 of 8.
+// 4000 x 5000 bf16 with 5 alternatives 27.2 us in CTAs of 4 warps, 33.0 of 8.
 // Rows up to four times as long as 8 warps' chunks are taken by 4 warps while they
-// fill the SMs (3000 x 16000 with 5: 38.7 us, 46.8 with 8), others by 8.  The rows left
+// fill the SMs (3000 x 16000 with 5: 38.9 us, 46.9 with 8), others by 8.  The rows left
 // when all others fill the SMs take a launch of their own, on what the ones before leave
 // free, in clusters as large as still fit at once, while a warp has more than a
 // chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without

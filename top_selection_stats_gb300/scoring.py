@@ -6,6 +6,10 @@ Every tensor lives on the logits' (the hidden states') CUDA device and is
 contiguous; the calls run on that device's current stream.  ``out`` takes what
 an earlier call of the same shape returned and writes it again, so a serving
 loop allocates nothing (head_logprobs: with ``workspace`` as well).
+
+The results carry no autograd history, whatever the arguments require: a loss
+differentiates them through a torch.autograd.Function around token_logprobs and
+token_logprobs_grad, as examples/policy_step.py has it.
 """
 import torch
 
@@ -112,7 +116,9 @@ def token_logprobs_grad(logits, targets, stats, grad_logprobs=None, entropy=None
     dtype and shape, for d loss / d logprobs = grad_logprobs and d loss /
     d entropy = grad_entropy (float32 [B], either None).  stats and entropy are
     the forward call's.  ``out`` may be logits itself (in place); columns past
-    V are zero in a fresh result and are not written in ``out``."""
+    V are zero in a fresh result and are not written in ``out``.  Logits that start
+    inside a 16-byte unit (a slice of rows of odd length) take 2 to 4 times as long
+    into a result that does not, a fresh one among them."""
     L = lib or load_library()
     B, ld = _matrix(logits, "logits", _DTYPES)
     V = _width(V, ld, "V")
