@@ -437,6 +437,9 @@ constexpr int HJOIN = 128;
 __global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, int ctas) {
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ float4 sw[HJOIN / 32];
+  asm volatile("griddepcontrol.launch_dependents;");  // a next call's head_kernel may get ready
+  // head_kernel's states are complete, and what was written before it is visible here too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float T = a.temperature ? a.temperature[row] : 1.f;
   const int t = a.targets ? a.targets[row] : -1;
   const bool valid = sc_temperature_ok(T) && t >= -1 && t < a.V;
@@ -444,8 +447,6 @@ __global__ void __launch_bounds__(HJOIN) head_join(const HeadArgs a, int parts, 
   Soft st{-INFINITY, 0.f, 0.f};
   float xt = -INFINITY;
   bool bad = false, late = false;
-  asm volatile("griddepcontrol.launch_dependents;");  // a next call's head_kernel may get ready
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // head_kernel's states are complete
   for (int c = tid; c < ctas; c += HJOIN) late |= reinterpret_cast<const int*>(a.part)[c] != 0;
   const float4* part = a.part + HFLAGS / 4 + (size_t)row * parts;
   for (int c = tid; c < parts; c += 8 * HJOIN) {
