@@ -11,8 +11,8 @@
 // each with half of the tile's columns, read finished accumulators into
 // registers: a thread owns one state's half row, folds it into a softmax state
 // {m, S, U} and writes that to the workspace with the target's logit.
-// 4096 x 128256 x 4096 bf16: 2393-2453 us, 1.76 PFLOP/s under the power limit; on
-// single CTAs (128 x 256, half as much again from L2) 2563.  One state: 159.6
+// 4096 x 128256 x 4096 bf16: 2360-2440 us, 1.8 PFLOP/s under the power limit; on
+// single CTAs (128 x 256, half as much again from L2) 2563.  One state: 158-159
 // us, 6.6 TB/s of weights, with 10 stages of 32 state rows; 163.4 with 6 of 128.
 //
 // The tensor cores' binary32 accumulation drops low bits instead of rounding:

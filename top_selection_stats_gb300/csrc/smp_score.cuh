@@ -1,6 +1,6 @@
 // smp_score.cuh -- what the scoring kernels (smp_score_kernel.cuh,
-// smp_score_grad.cu, smp_head.cu) share: the softmax state of a set of values, its merge, and
-// the results computed from it.
+// smp_score_grad.cu, smp_head.cu) share: the softmax state of a set of values,
+// its merge, the results computed from it, and bounded waits.
 //
 // A set A of values x with largest m, scaled by s = log2(e) / T, is held as
 //     m,  S = sum 2^d,  U = sum 2^d d,   d = (x - m) s <= 0,

@@ -631,7 +631,8 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       for (int i = 0; i < SFIRST; ++i) above += firsts[i] > v || (firsts[i] == v && i < tid);
       if (above == n - 1) sh.low = max(v, 1u);  // 0: fewer than n; any legal value
     }
-    const bool late = __syncthreads_or(bad & SC_LATE);  // the row fails: not all buckets are there, nothing to search
+    // a CTA with a late copy has not all its buckets, and its row fails: it searches nothing
+    const bool late = __syncthreads_or(bad & SC_LATE);
     const uint32_t low = sh.low;
     uint64_t bound = (uint64_t)low << 32;
     auto offer = [&](float y, int j) {
@@ -806,10 +807,10 @@ int launch_score(const ScoreArgs& a, int r0, int rows, int nc, cudaStream_t st) 
 // fill the SMs (3000 x 16000 with 5: 38.9 us, 46.9 with 8), others by 8.  The rows left
 // when all others fill the SMs take a launch of their own, on what the ones before leave
 // free, in clusters as large as still fit at once, while a warp has more than a
-// chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without
-// it; 64 x 128256 bf16 with 20: 10.1 us in clusters of 4, 14.7 of 8 (two
-// rounds of CTAs).  So a call is one launch, two or, where rows of up to four times 8
-// warps' chunks leave at least a full round of CTAs of 8 warps, three.
+// chunk: 1024 x 256000 f16 with 32 alternatives 105 us, 112 without it; 64 x 128256
+// bf16 with 20: 10.1 us in clusters of 4, 14.7 of 8 (two rounds of CTAs).  So a call
+// is one launch, two or, where rows of up to four times 8 warps' chunks leave at least a
+// full round of CTAs of 8 warps, three.
 template <int DT>
 int score_rows(const ScoreArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
