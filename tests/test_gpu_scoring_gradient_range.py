@@ -77,6 +77,11 @@ def test_sizes_of_the_incoming_gradient(size, entropy):
           entropy, size, False)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_results_aligned_unlike_their_logits(dtype):
+    check(T.make(20, 3001, dtype, 6, shift=1, masked=True, temps=TEMPS, grid=2, neg_inf=0.05), dtype, True, 1.0, False)
+
+
 def test_far_rows_beside_others():
     """A row out of range leaves its neighbours' bits alone."""
     c = T.make(6, 5003, "bf16", 5, temps=[1.0])
