@@ -396,8 +396,126 @@ int smp_head_logprobs(const void* hidden, int64_t ld_hidden, const void* weight,
  * for N or V < 1). */
 int64_t smp_head_workspace(int N, int V);
 
-/* Bounds the device-side waits of smp_token_logprobs and smp_head_logprobs calls
- * made from now on, by any thread, to `cycles` SM clock cycles (<= 0: the
+/* ---- Processing of logits ------------------------------------------------
+ * Penalties for repeated tokens, biases and a grammar mask, in one call, before
+ * sampling ("Sampling system design" post, section on logits processors).  No
+ * handle, no allocation; runs on the CURRENT CUDA device, on `stream`.  For row r
+ * and token j, with n_j the copies of j among the row's generated tokens:
+ *   1. j in the history (prompt or generated): x_j / repetition[r] if x_j > 0,
+ *      else x_j * repetition[r];
+ *   2. minus frequency[r] * n_j, and minus presence[r] if n_j > 0;
+ *   3. plus each bias whose id is j, in slot order (-inf bans the token);
+ *   4. -inf if the bitmask's bit j is 0;
+ * computed in binary32, rounded once to `out_dtype` (to nearest even; 16-bit
+ * results past the type's range are infinities).  Steps without their arguments
+ * are left out.
+ *   logits    : DEVICE [B][ld] of dtype.
+ *   history   : DEVICE int32 [B][history_ld], H entries per row, the prompt's
+ *               tokens first, then the generated ones; NULL allowed when H == 0.
+ *               Entries outside [0, V) are padding.
+ *   lengths, prompt_lengths: DEVICE int32 [B], nullable: how many entries row r
+ *               has (NULL: H), and how many of them are its prompt (NULL: 0).
+ *   repetition, presence, frequency: DEVICE float [B], each nullable (1, 0, 0).
+ *   bias_ids  : DEVICE int32 [B][NB], bias: DEVICE float [B][NB]; NULL allowed
+ *               when NB == 0.  Ids outside [0, V) are unused slots.
+ *   bitmask   : DEVICE uint32 [B][ceil(V/32)], nullable.
+ *   out       : DEVICE [B][out_ld] of out_dtype (dtype, or SMP_F32); columns from
+ *               V on are not written.  May be the logits themselves (same
+ *               pointer, type and ld): the call then touches only what changes.
+ *               Any other overlap of the two is not allowed.
+ *   row_status: DEVICE int32 [B], required.  SMP_ERR_INVALID_PARAM: a repetition
+ *               that is not finite and > 0, a presence or frequency that is not
+ *               finite, a length outside [0, H], a prompt length outside [0,
+ *               length], or a bias in a used slot that is NaN or +inf; the row
+ *               then goes through unchanged, without its mask.
+ * Logits that are NaN stay NaN, -inf stays -inf (a negative or NaN logit that is
+ * masked becomes -inf).
+ * Call status: SMP_ERR_INVALID_PARAM for NULL required pointers, B < 0, V < 1,
+ * ld < V, out_ld < V, H < 0, history_ld < H, NB < 0, an out_dtype that is neither
+ * dtype nor SMP_F32, or out == logits with another type or ld; SMP_ERR_CAPACITY
+ * for V or H above 16,777,216 or NB above 4096; SMP_ERR_CUDA when the launch
+ * fails. */
+int smp_process_logits(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
+                       const int32_t* history, int H, int64_t history_ld, const int32_t* lengths,
+                       const int32_t* prompt_lengths, const float* repetition,
+                       const float* presence, const float* frequency, const int32_t* bias_ids,
+                       const float* bias, int NB, const uint32_t* bitmask, void* out,
+                       smp_dtype out_dtype, int64_t out_ld, int32_t* row_status,
+                       smp_stream stream);
+
+/* ---- Distillation from a teacher's top tokens -----------------------------
+ * The divergence of a student's distribution p = softmax(x / T) over its legal
+ * tokens from a teacher known by K of its tokens (for example the alternatives
+ * that smp_token_logprobs returns for the teacher's logits), and its gradient.
+ * Same conventions as the scoring calls above (temperature, bitmask, targets,
+ * alignment, status, waits).  With slots k = 0..K-1 of distinct token ids, q_k
+ * the teacher's and p_k the student's probability of slot k's token,
+ * s = the student's mass outside the slots, r = max(1 - sum q_k, 2^-24):
+ *   SMP_DISTILL_FORWARD  : sum q_k (log q_k - log p_k) + r (log r - log s)
+ *   SMP_DISTILL_REVERSE  : sum p_k (log p_k - log q_k) + s (log s - log r)
+ *   SMP_DISTILL_TRUNCATED: sum q_k (log q_k - log p_k), q = softmax over the
+ *                          slots of teacher / T
+ * (the first two: all other tokens are one class, and `teacher` holds log
+ * probabilities; in the third it holds logits, at temperature 1, and the rest of
+ * the teacher's distribution is left out).  When no legal token lies outside the
+ * slots, the terms with r and s are 0.  Terms with weight 0 are 0; a slot of
+ * weight > 0 whose other probability is 0 makes the loss +inf, and such a row has
+ * no gradient of its loss.
+ *   teacher_ids : DEVICE int32 [B][K], 1 <= K <= 256: token ids, -1 for an unused
+ *                 slot.  A row without a used slot has loss 0 and no gradient.
+ *   teacher     : DEVICE float [B][K]; -inf: probability 0.
+ *   targets     : DEVICE int32 [B] or NULL: tokens whose log probability is wanted
+ *                 beside the divergence, as in smp_token_logprobs.
+ * Outputs, DEVICE:
+ *   loss         : float [B], required.
+ *   logprobs     : float [B]: log p of the target; required with targets.
+ *   slot_logprobs: float [B][K], nullable: log p_k; -inf for unused slots.
+ *   slot_grads   : float [B][K], nullable: T times the loss's derivative by the
+ *                  slot's logit; 0 for unused slots.
+ *   stats        : float [B][4], nullable: {m, L, A, s}: the largest logit outside
+ *                  the slots, log of the mass there relative to it, the factor of
+ *                  the loss's derivative there, and s.  The last three arrays are
+ *                  what smp_distill_loss_grad takes.
+ *   row_status   : int32 [B], required.  As in the scoring calls, and
+ *                  SMP_ERR_INVALID_PARAM also for an id outside [-1, V), the same id
+ *                  in two slots, or (not TRUNCATED) sum q_k > 1 + 2^-10;
+ *                  SMP_ERR_NONFINITE also for a teacher value in a used slot that
+ *                  is NaN or +inf.
+ * A row whose status is not SMP_OK gets NaN in all float outputs.
+ * Call status: SMP_ERR_INVALID_PARAM for NULL required pointers, B < 0, V < 1,
+ * ld < V, K < 1, an unknown dtype or kind; SMP_ERR_CAPACITY for K > 256 or V >
+ * 16,777,216; SMP_ERR_CUDA when the launch fails.  Work: one read of the logits. */
+enum { SMP_DISTILL_FORWARD = 0, SMP_DISTILL_REVERSE = 1, SMP_DISTILL_TRUNCATED = 2 };
+int smp_distill_loss(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
+                     const uint32_t* bitmask, const float* temperature, const int32_t* teacher_ids,
+                     const float* teacher, int K, int kind, const int32_t* targets, float* loss,
+                     float* logprobs, float* slot_logprobs, float* slot_grads, float* stats,
+                     int32_t* row_status, smp_stream stream);
+
+/* Gradient of smp_distill_loss' loss and logprobs with respect to the logits, for
+ * a training loss with d / d loss[r] = grad_loss[r] and d / d logprobs[r] =
+ * grad_logprobs[r], computed in binary32 and rounded once to `dtype`; 0 for tokens
+ * that are not legal and in rows that failed.  grad_logprobs counts nothing in a
+ * row without a target or with one that is not legal.
+ *   logits, bitmask, temperature, teacher_ids, K, targets: as given to the forward
+ *                   call (of any kind).
+ *   slot_logprobs, slot_grads, stats, logprobs: the forward call's; slot_logprobs,
+ *                   logprobs and targets are needed with grad_logprobs only.
+ *   grad_loss, grad_logprobs: DEVICE float [B], either may be NULL (zero).
+ *   grad          : [B][grad_ld] of dtype, grad_ld >= V; columns from V on are not
+ *                   written.  May be the logits themselves (same pointer and ld).
+ * Call status as for smp_distill_loss.  Work: one read of the logits and one write
+ * of the gradient. */
+int smp_distill_loss_grad(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
+                          const uint32_t* bitmask, const float* temperature,
+                          const int32_t* teacher_ids, int K, const float* slot_logprobs,
+                          const float* slot_grads, const float* stats, const float* grad_loss,
+                          const int32_t* targets, const float* logprobs,
+                          const float* grad_logprobs, void* grad, int64_t grad_ld,
+                          smp_stream stream);
+
+/* Bounds the device-side waits of smp_token_logprobs, smp_head_logprobs and
+ * smp_distill_loss calls made from now on, by any thread, to `cycles` SM clock cycles (<= 0: the
  * default, 4e9, about two seconds; a captured graph keeps the bound it was
  * captured with).  A wait that runs out gives SMP_ERR_TIMEOUT for its row, in
  * smp_head_logprobs for all rows of the call.  Always SMP_OK. */

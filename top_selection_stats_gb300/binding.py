@@ -20,7 +20,8 @@ EXPORTS = ("smp_create", "smp_destroy", "smp_topk_topp_mask", "smp_sample", "smp
            "smp_repetition_penalty", "smp_gumbel_sample", "smp_top_logprobs", "smp_set_row_info",
            "smp_set_kernel", "smp_set_wait_limit", "smp_plan", "smp_token_logprobs",
            "smp_token_logprobs_grad", "smp_head_logprobs", "smp_head_workspace",
-           "smp_set_scoring_wait_limit",
+           "smp_set_scoring_wait_limit", "smp_process_logits", "smp_distill_loss",
+           "smp_distill_loss_grad",
            "smp_status_string")
 
 
@@ -78,6 +79,9 @@ def load_library(path=None):
     L.smp_head_workspace.argtypes = [I, I]
     L.smp_head_workspace.restype = I64
     L.smp_set_scoring_wait_limit.argtypes = [ctypes.c_longlong]
+    L.smp_process_logits.argtypes = [P, I, I, I, I64, P, I, I64, P, P, P, P, P, P, P, I, P, P, I, I64, P, P]
+    L.smp_distill_loss.argtypes = [P, I, I, I, I64, P, P, P, P, I, I, P, P, P, P, P, P, P, P]
+    L.smp_distill_loss_grad.argtypes = [P, I, I, I, I64, P, P, P, I, P, P, P, P, P, P, P, P, I64, P]
     L.smp_status_string.restype = ctypes.c_char_p
     L.smp_status_string.argtypes = [I]
     for name in EXPORTS:

@@ -4,7 +4,7 @@
 #include <atomic>
 #include <cstdint>
 
-#include "smp_score.cuh"
+#include "smp_train.cuh"
 
 using namespace smp;
 
@@ -14,6 +14,10 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) !
 constexpr int HEAD_MAX = 1 << 20;
 std::atomic<long long> g_wait_limit{SC_WAIT};
 }  // namespace
+
+namespace smp {
+long long scoring_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+}  // namespace smp
 
 extern "C" {
 

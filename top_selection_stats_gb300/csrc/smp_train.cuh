@@ -1,0 +1,63 @@
+// smp_train.cuh -- arguments and entry points of the processing and distillation
+// calls (smp_process.cu, smp_distill.cu, smp_distill_grad.cu, smp_train_api.cu).
+#pragma once
+
+#include "smp_score.cuh"
+
+namespace smp {
+
+constexpr int DI_MAX_K = 256;         // slots of a teacher
+constexpr int PR_MAX_H = 1 << 24;     // history entries: counts are exact in binary32
+constexpr int PR_MAX_NB = 4096;       // biases of a row
+constexpr float DI_LEAST = 0x1p-24f;  // the teacher's mass outside its slots, at least
+constexpr double DI_MOST = 1.0 + 0x1p-10;  // the sum of a teacher's probabilities, at most
+
+struct ProcessArgs {
+  const void* logits;
+  long long ld;
+  const int32_t* history;
+  long long hld;
+  const int32_t *lengths, *prompts;
+  const float *repetition, *presence, *frequency;
+  const int32_t* bias_ids;
+  const float* bias;
+  const uint32_t* bitmask;
+  void* out;
+  long long old;
+  int32_t* status;
+  int B, V, W, H, NB;
+};
+struct DistillArgs {
+  const void* logits;
+  long long ld;
+  const uint32_t* bitmask;
+  const float* temperature;
+  const int32_t* ids;
+  const float* teacher;
+  const int32_t* targets;
+  float *loss, *logprobs, *slot_lp, *slot_g, *stats;
+  int32_t* status;
+  int B, V, W, K, kind;
+  long long wait_limit;
+};
+struct DistillGradArgs {
+  const void* logits;
+  long long ld, gld;
+  const uint32_t* bitmask;
+  const float* temperature;
+  const int32_t* ids;
+  const float *slot_lp, *slot_g, *stats, *g_loss;
+  const int32_t* targets;
+  const float *logprobs, *g_lp;
+  void* grad;
+  int B, V, W, K;
+};
+
+int process_enqueue(const ProcessArgs& a, int dtype, int out_dtype, cudaStream_t st);
+int distill_enqueue(const DistillArgs& a, int dtype, cudaStream_t st);
+int distill_grad_enqueue(const DistillGradArgs& a, int dtype, cudaStream_t st);
+
+// The bound that smp_set_scoring_wait_limit holds (smp_score_api.cu).
+long long scoring_wait_limit();
+
+}  // namespace smp

@@ -1,0 +1,82 @@
+"""Penalties for repeated tokens, biases and grammar masks on logits before they are
+sampled from (smp_process_logits, a handle-free call of include/smp.h).  Argument
+marshalling only; the conventions are scoring.py's.
+"""
+import math
+
+import torch
+
+from .binding import _DTYPES, _check, load_library
+from .scoring import _F32, _I32, _bitmask, _current_device, _matrix, _need, _opt, _raw_stream, _width
+
+
+def process_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None, presence=None,
+                   frequency=None, bias_ids=None, bias=None, bitmask=None, V=None, dtype=None, in_place=False,
+                   out=None, lib=None):
+    """smp_process_logits: per row of logits [B, V] (or [B, ld] with ``V``), in this order,
+
+    * repetition penalty (float32 [B]) on every token of the row's history: positive
+      logits divided, others multiplied by it;
+    * frequency (float32 [B]) times a token's copies among the generated tokens, and presence
+      (float32 [B]) if it has any, subtracted;
+    * biases added: bias float32 [B, NB] at token ids bias_ids int32 [B, NB] (outside [0, V):
+      unused; -inf bans a token);
+    * -inf where bitmask (int32 [B, ceil(V/32)]) has a 0.
+
+    history: int32 [B, H], the prompt's tokens first; lengths, prompt_lengths: int32 [B], the
+    entries that a row has (None: H) and how many of them are its prompt (None: 0).  The result
+    has the logits' dtype, or float32 with ``dtype=torch.float32``.  ``in_place`` changes the
+    logits themselves and touches nothing else of them.  Returns logits and status.  ``out``
+    takes what an earlier call of the same shape returned; columns past V are -inf in a fresh
+    result and are not written otherwise.  Rows with an invalid parameter go through unchanged."""
+    L = lib or load_library()
+    B, ld = _matrix(logits, "logits", _DTYPES)
+    V = _width(V, ld, "V")
+    dev = logits.get_device()
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return process_logits(logits, history, lengths, prompt_lengths, repetition, presence, frequency, bias_ids,
+                                  bias, bitmask, V, dtype, in_place, out, lib)
+    dtype = logits.dtype if dtype is None else dtype
+    if dtype is not logits.dtype and (dtype is not _F32 or in_place):
+        raise ValueError(f"results of {logits.dtype} logits cannot be {dtype}" + (" in place" if in_place else ""))
+    H = hist = NB = ids = b = None
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != B:
+            raise ValueError("history must be [B, H]")
+        H = history.shape[1]
+        hist = _need(history, "history", dev, _I32, B * H)
+    elif lengths is not None or prompt_lengths is not None:
+        raise ValueError("lengths and prompt_lengths need a history")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None:
+        if bias.dim() != 2 or bias.shape[0] != B or bias_ids.shape != bias.shape:
+            raise ValueError("bias_ids and bias must be [B, NB]")
+        NB = bias.shape[1]
+        ids, b = _need(bias_ids, "bias_ids", dev, _I32, B * NB), _need(bias, "bias", dev, _F32, B * NB)
+    if out is None:
+        status = torch.empty(B, dtype=_I32, device=logits.device)
+        if in_place:
+            result = logits
+        else:
+            result = torch.empty((B, ld), dtype=dtype, device=logits.device)
+            if V < ld:
+                result[:, V:].fill_(-math.inf)
+        out = dict(logits=result, status=status)
+    else:
+        result = logits if in_place else out["logits"]
+        if result.dim() != 2 or result.shape[0] != B or result.shape[1] < V:
+            raise ValueError(f"out must be [{B}, at least {V}], got {list(result.shape)}")
+        if in_place:
+            out["logits"] = logits
+    to = _need(result, "out", dev, dtype, result.numel())
+    rc = L.smp_process_logits(logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, hist, H or 0, H or 0,
+                              _opt(lengths, "lengths", dev, _I32, B),
+                              _opt(prompt_lengths, "prompt_lengths", dev, _I32, B),
+                              _opt(repetition, "repetition", dev, _F32, B), _opt(presence, "presence", dev, _F32, B),
+                              _opt(frequency, "frequency", dev, _F32, B), ids, b, NB or 0,
+                              _bitmask(bitmask, dev, B, V), to, _DTYPES[dtype], result.shape[1],
+                              _need(out["status"], "status", dev, _I32, B), _raw_stream(dev))
+    _check(rc, "smp_process_logits")
+    return out
