@@ -20,13 +20,14 @@ SOURCES = [os.path.join(CSRC, f) for f in ("smp_api.cu", "smp_k_f32.cu", "smp_k_
                                            "smp_score_f32.cu", "smp_score_bf16.cu",
                                            "smp_score_f16.cu", "smp_score_grad.cu",
                                            "smp_head.cu", "smp_train_api.cu", "smp_process.cu",
-                                           "smp_distill.cu", "smp_distill_grad.cu")]
+                                           "smp_distill_f32.cu", "smp_distill_bf16.cu",
+                                           "smp_distill_f16.cu", "smp_distill_grad.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("smp_philox.cuh", "smp_device.cuh", "smp_core.cuh",
                                            "smp_list.cuh",
                                            "smp_stream_passes.cuh", "smp_general.cuh",
                                            "smp_kernel.cuh", "smp_split.cuh", "smp_score.cuh",
                                            "smp_score_kernel.cuh", "smp_train.cuh",
-                                           "smp_distill.cuh")]
+                                           "smp_distill.cuh", "smp_distill_kernel.cuh")]
 DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", "smp.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

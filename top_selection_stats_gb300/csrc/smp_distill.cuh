@@ -21,14 +21,7 @@
 namespace smp {
 namespace {
 
-constexpr int DI_PER_LANE = DI_MAX_K / 32;
-
 __device__ __forceinline__ float di_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ double di_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -39,14 +32,22 @@ __device__ __forceinline__ float di_max(float v) {
   return v;
 }
 
-// One warp: the row's results.  rest: the state of the legal tokens outside the
-// slots; ids, xk: the slots' ids (negative: unused) and logits (-inf: not legal), in
-// shared memory, K of each; xt: the target's logit (-inf: not legal); wrong: what was
-// found so far.
 enum { DI_INVALID = 1, DI_NONFINITE = 2, DI_LATE = 4 };
 
+// A row's slots in shared memory.
+struct Slots {
+  int ids[DI_MAX_K];       // negative: unused
+  float x[DI_MAX_K];       // the student's logit, -inf: not legal
+  float teacher[DI_MAX_K];  // -inf in unused slots
+};
+
+// One warp: the row's results.  rest: the state of the legal tokens outside the
+// slots; total: the sum of the teacher's probabilities (not truncated); xt: the target's
+// logit (-inf: not legal); wrong: what was found so far.
 __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, float T, int t, float xt, int wrong,
-                                               float rest_m, float rest_S, const int* ids, const float* xk) {
+                                               float rest_m, float rest_S, const Slots& slots, double total) {
+  const int* ids = slots.ids;
+  const float *xk = slots.x, *teacher = slots.teacher;
   const int lane = threadIdx.x & 31, K = a.K;
   const size_t at = (size_t)r * K;
   const float s_scale = sc_scale(wrong & DI_INVALID ? 1.f : T);
@@ -67,27 +68,16 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
   const float mass = bare ? 0.f : expf(log_s);
   // the teacher
   float top = -INFINITY, size = 0.f;
-  double total = 0.0;
-  for (int k = lane; k < K; k += 32) {
-    if (ids[k] < 0) continue;
-    const float v = a.teacher[at + k];
-    if (!(v < INFINITY)) {
-      wrong |= DI_NONFINITE;
-      continue;
-    }
-    top = fmaxf(top, v);
-    if (a.kind != SMP_DISTILL_TRUNCATED) total += exp((double)v);
-  }
   float Q, rest = 0.f, log_size = 0.f;
   if (a.kind == SMP_DISTILL_TRUNCATED) {
+    for (int k = lane; k < K; k += 32) top = fmaxf(top, teacher[k]);
     top = di_max(top);
     for (int k = lane; k < K; k += 32)
-      if (ids[k] >= 0 && top > -INFINITY) size += expf(__fdiv_rn(a.teacher[at + k] - top, T));
+      if (teacher[k] > -INFINITY) size += expf(__fdiv_rn(teacher[k] - top, T));
     size = di_sum(size);
     log_size = logf(size);
     Q = top > -INFINITY ? 1.f : 0.f;
   } else {
-    total = di_sum(total);
     if (total > DI_MOST) wrong |= DI_INVALID;
     Q = (float)total;
     if (!bare) rest = fmaxf((float)(1.0 - total), DI_LEAST);
@@ -103,11 +93,8 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
   auto slot = [&](int k, float& lp, float& p, float& lq, float& q) {
     lp = xk[k] == -INFINITY ? -INFINITY : fminf(__fdiv_rn(xk[k] - m, T) - L, 0.f);
     p = expf(lp);
-    lq = -INFINITY;
-    if (ids[k] >= 0) {
-      lq = a.teacher[at + k];
-      if (a.kind == SMP_DISTILL_TRUNCATED) lq = lq == -INFINITY ? lq : __fdiv_rn(lq - top, T) - log_size;
-    }
+    lq = teacher[k];
+    if (a.kind == SMP_DISTILL_TRUNCATED && lq > -INFINITY) lq = __fdiv_rn(lq - top, T) - log_size;
     q = expf(lq);
   };
   float loss = 0.f;

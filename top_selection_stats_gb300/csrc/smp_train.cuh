@@ -1,5 +1,6 @@
 // smp_train.cuh -- arguments and entry points of the processing and distillation
-// calls (smp_process.cu, smp_distill.cu, smp_distill_grad.cu, smp_train_api.cu).
+// calls (smp_process.cu, smp_distill_kernel.cuh, smp_distill_grad.cu,
+// smp_train_api.cu).
 #pragma once
 
 #include "smp_score.cuh"
@@ -54,7 +55,9 @@ struct DistillGradArgs {
 };
 
 int process_enqueue(const ProcessArgs& a, int dtype, int out_dtype, cudaStream_t st);
-int distill_enqueue(const DistillArgs& a, int dtype, cudaStream_t st);
+int distill_f32(const DistillArgs& a, cudaStream_t st);
+int distill_bf16(const DistillArgs& a, cudaStream_t st);
+int distill_f16(const DistillArgs& a, cudaStream_t st);
 int distill_grad_enqueue(const DistillGradArgs& a, int dtype, cudaStream_t st);
 
 // The bound that smp_set_scoring_wait_limit holds (smp_score_api.cu).

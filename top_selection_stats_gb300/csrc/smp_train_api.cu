@@ -81,7 +81,8 @@ int smp_distill_loss(const void* logits, smp_dtype dtype, int B, int V, int64_t 
   a.K = K;
   a.kind = kind;
   a.wait_limit = scoring_wait_limit();
-  return distill_enqueue(a, (int)dtype, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  return dtype == SMP_F32 ? distill_f32(a, st) : dtype == SMP_BF16 ? distill_bf16(a, st) : distill_f16(a, st);
 }
 
 int smp_distill_loss_grad(const void* logits, smp_dtype dtype, int B, int V, int64_t ld,
