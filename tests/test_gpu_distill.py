@@ -91,7 +91,9 @@ def errors(o, V, T, kind):
     """Bounds for a row's results, from the module's docstring."""
     with np.errstate(invalid="ignore", over="ignore"):
         eL = U * (4 * o["zbar"] + 4 * o["L"] + V / 256 + 80)
-        eR = 0.0 if o["stats"][3] == 0 else U * (4 * o["zbar_r"] + 4 * abs(o["stats"][1]) + V / 256 + 80)
+        # the bound holds for any mass outside the slots, one that binary64 shows as s = 0 among
+        # them (its logarithm is relative to its own largest value); there is none in a bare row
+        eR = 0.0 if not o["outside"].any() else U * (4 * o["zbar_r"] + 4 * abs(o["stats"][1]) + V / 256 + 80)
         live = o["slot_logprobs"] > -np.inf
         ek = np.where(live, eL + eR + 8 * U + 4 * U * np.where(live, np.abs(o["slot_logprobs"]) + o["L"], 0.0), 0.0)
         es = eL + eR + 8 * U + (4 * U * (abs(o["log_s"]) + o["L"] + abs(o["stats"][1])) if o["stats"][3] > 0 else 0.0)

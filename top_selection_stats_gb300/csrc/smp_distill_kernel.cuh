@@ -19,6 +19,7 @@ namespace smp {
 namespace {
 
 constexpr int DI_STAGES = 2;  // chunks a warp has in flight
+constexpr float DI_NEAR = 1.0e30f;
 
 struct DistillPart {
   float m, S;
@@ -28,18 +29,21 @@ struct DistillPart {
 template <int ST>
 struct DistillScratch {
   Slots slots;
+  RowResult row;
   uint64_t full[ST / 32 * DI_STAGES];
-  double total[ST / 32];
+  int seen[DI_MAX_K * 2];  // ids by open addressing; more than 32 slots
   DistillPart part[SMAXC];  // first CTA: the states of all
-  DistillPart warp[ST / 32];
+  DistillPart warp[ST / 32 + 1];
 };
 
 // cv: vectors of a chunk, a multiple of 32, at most 32 << SLNU.
-template <int DT, int ST, bool MASK>
-__global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
+// EXTRA: one more warp takes the slots and finishes the row, while the others stream from the
+// start; without it all warps share the slots first.
+template <int DT, int ST, bool MASK, bool EXTRA>
+__global__ void __launch_bounds__(ST + (EXTRA ? 32 : 0), ST == 64 ? SSMALL : SROWS * 256 / ST)
     distill_kernel(const DistillArgs a, const int row_ctas, const int seg, const int cv, const int r0,
                    const bool more) {
-  const int nc = ST == 256 ? row_ctas : 1;
+  const int nc = ST == 256 && !EXTRA ? row_ctas : 1;
   using TY = ScType<DT>;
   using raw = typename TY::raw;
   using WD = Word<DT>;
@@ -48,6 +52,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   constexpr int NU = 1 << SLNU;  // vectors of a lane in a chunk, at most
   constexpr int CV = 32 * NU;
   constexpr int NW = CV * VE / 1024;  // mask words of a lane
+  constexpr int WF = EXTRA ? SW : 0;  // the warp that finishes the row
   __shared__ __align__(16) DistillScratch<ST> sh;
   extern __shared__ __align__(128) uint8_t ring_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K;
@@ -64,7 +69,8 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   const int v0 = min(f1, f0 + rank_c * seg), v1 = min(f1, v0 + seg);
   const uint4* src = reinterpret_cast<const uint4*>(row - lead);
   const int mine = v0 + warp * cv;  // this warp's first chunk; the next is SW * cv further
-  const int chunks = max(0, (v1 - mine + SW * cv - 1) / (SW * cv));
+  const bool streams = !EXTRA || warp < SW;
+  const int chunks = streams ? max(0, (v1 - mine + SW * cv - 1) / (SW * cv)) : 0;
   uint4* ring = reinterpret_cast<uint4*>(ring_raw) + warp * (DI_STAGES * cv);
   uint64_t* full = sh.full + warp * DI_STAGES;
   // Chunk i into its stage; what it does not fill holds nothing, written by the lane that
@@ -80,12 +86,15 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
       bulk_g2s(stage, src + c, k * 16, &full[i % DI_STAGES]);
     }
   };
-  if (lane == 0) {
+  if (lane == 0 && streams) {
     for (int i = 0; i < DI_STAGES; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  __syncwarp();
+  if (rank_c == 0 && K > 32)
+    for (int i = EXTRA ? lane : tid; i < 2 * DI_MAX_K && (!EXTRA || warp == SW); i += EXTRA ? 32 : ST) sh.seen[i] = -1;
+  if (EXTRA) __syncwarp();
+  else __syncthreads();
   // The launches of a call follow each other, and the work before them, as those of
   // smp_token_logprobs do.
   if (r0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -105,41 +114,31 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   int wrong = sc_temperature_ok(T) && t >= -1 && t < a.V ? 0 : DI_INVALID;
   const float s = sc_scale(wrong ? 1.f : T);
   const float xt = rank_c == 0 && !wrong && t >= 0 && legal(t) ? TY::value(row[t]) : -INFINITY;
-  double total = 0.0;
-  for (int k = tid; k < K; k += ST) {
-    const size_t at = (size_t)r * K + k;
-    const int id = a.ids[at];
-    const bool in = id >= 0 && id < a.V;
-    if (!in && id != -1) wrong |= DI_INVALID;
-    sh.slots.ids[k] = in ? id : -1;
-    if (rank_c == 0) {
-      float v = in ? a.teacher[at] : -INFINITY;
-      const float x = in && legal(id) ? TY::value(row[id]) : -INFINITY;
-      if (!(v < INFINITY)) {
-        wrong |= DI_NONFINITE;
-        v = -INFINITY;
+  // the slots, 32 to a warp; those past the last are unused
+  for (int k0 = EXTRA ? 0 : warp * 32; k0 < K && (!EXTRA || warp == SW); k0 += EXTRA ? 32 : ST) {
+    const int k = k0 + lane, given = k < K ? a.ids[(size_t)r * K + k] : -1;
+    const int id = given >= 0 && given < a.V ? given : -1;
+    if (id != given) wrong |= DI_INVALID;
+    sh.slots.ids[k] = id;
+    if (rank_c) continue;
+    const float v = id >= 0 ? a.teacher[(size_t)r * K + k] : -INFINITY;
+    const float x = id >= 0 && legal(id) ? TY::value(row[id]) : -INFINITY;
+    // the same id twice
+    if (K <= 32) {
+      if ((__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1)) && id >= 0) wrong |= DI_INVALID;
+    } else if (id >= 0) {
+      for (unsigned h = (unsigned)id * 2654435761u >> 23;; ++h) {  // 512 entries, at most 256 ids
+        const int old = atomicCAS(&sh.seen[h & (2 * DI_MAX_K - 1)], -1, id);
+        if (old == id) wrong |= DI_INVALID;
+        if (old == -1 || old == id) break;
       }
-      sh.slots.teacher[k] = v;
-      sh.slots.x[k] = x;
-      if (a.kind != SMP_DISTILL_TRUNCATED) total += exp((double)v);
     }
+    distill_slots(a, sh.slots, k0, id, x, v, T, s);
   }
-  if (rank_c == 0) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) sh.total[warp] = total;
-  }
-  __syncthreads();
-  if (rank_c == 0) {
-    for (int k = tid; k < K; k += ST) {
-      const int id = sh.slots.ids[k];
-      bool twice = false;
-      for (int i = 0; i < k; ++i) twice |= sh.slots.ids[i] == id;
-      if (twice && id >= 0) wrong |= DI_INVALID;
-    }
-  }
+  if (EXTRA) __syncwarp();
+  else __syncthreads();
   float xe = -INFINITY;
-  if (rank_c == 0 && warp == 0) {
+  if (rank_c == 0 && warp == (EXTRA ? SW : 0)) {
     const int head = lead ? min(a.V, VE - lead) : 0, tail = max(head, f1 * VE - lead);
     uint32_t taken = 0u;  // lanes whose value has a slot
     for (int k = lane; k < K; k += 32) {
@@ -151,9 +150,11 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     if (j < a.V && !((taken >> lane) & 1u) && legal(j)) xe = TY::value(row[j]);
   }
 
-  // The lane's sums are relative to ref, which follows its largest value mx only
-  // when that has left it by a factor of 2^SLAG.
-  float ref = -INFINITY, mx = -INFINITY;
+  // The lane's sum is of 2^(x s - c): one fused operation a value, rounded once whatever c
+  // is.  c follows its largest value mx only when that has left it by a factor of 2^SLAG.
+  // Where x s would pass binary32 (far), the sum is of 2^((x - ref) s).
+  float ref = -INFINITY, c2 = 0.f, mx = -INFINITY;
+  bool far = false;  // of some lane of the warp
   f32x2 S2 = pair(0.f, 0.f);
   const f32x2 s2 = pair(s, s);
   uint4 x[NU];
@@ -161,10 +162,18 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(top));
     const bool raise = (top - ref) * s > SLAG;
     if (__any_sync(0xffffffffu, raise)) {
-      const float d = !raise ? 0.f : ref == -INFINITY ? SC_DMIN : (ref - top) * s;
-      const float e = sc_ex2(d);
-      S2 = mul2(S2, pair(e, e));
-      if (raise) ref = top;
+      if (raise) {
+        const float e = sc_ex2(ref == -INFINITY ? SC_DMIN : (ref - top) * s);
+        // from one reference to the other, as the sum is held: 2^(c - (top s)) is exact to a
+        // rounding where the products are
+        const float to = top * s;
+        const bool near = fabsf(to) < DI_NEAR && fabsf(c2) < DI_NEAR;
+        const float by = ref > -INFINITY && near ? sc_ex2(c2 - to) : e;
+        S2 = mul2(S2, pair(by, by));
+        ref = top;
+        c2 = to;
+      }
+      far = __any_sync(0xffffffffu, !(fabsf(c2) < DI_NEAR));
     }
   };
   for (int i = 0; i < chunks; ++i) {
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     raw* values = reinterpret_cast<raw*>(stage);
     bool wrote = false;
     for (int k = lane; k < K; k += 32) {
-      const unsigned d = (unsigned)(sh.slots.ids[k] - first);
+      const unsigned d = (unsigned)((EXTRA ? a.ids[(size_t)r * K + k] : sh.slots.ids[k]) - first);
       if (d < (unsigned)(cv * VE)) {
         if constexpr (DT == SMP_F32) values[d] = -INFINITY;
         else values[d] = (raw)(WD::NONE & 0xffffu);
@@ -241,18 +250,31 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     __syncwarp();  // the stage has been read: every lane's values have gone into its top
     fetch(i + DI_STAGES);
     follow(top);
-    const float base = ref == -INFINITY ? 0.f : -ref;
-    const f32x2 mm = pair(base, base);
+    if (!far) {
+      const f32x2 cc = pair(-c2, -c2);
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      if (u * 32 >= cv) break;
-      float f[VE];
-      sc_unpack<DT>(x[u], f);
+      for (int u = 0; u < NU; ++u) {
+        if (u * 32 >= cv) break;
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
 #pragma unroll
-      for (int e = 0; e < VE; e += 2) {
-        float d0, d1;
-        unpair(mul2(add2(pair(f[e], f[e + 1]), mm), s2), d0, d1);
-        S2 = add2(S2, pair(sc_ex2(d0), sc_ex2(d1)));
+        for (int e = 0; e < VE; e += 2) {
+          float d0, d1;
+          unpair(fma2(pair(f[e], f[e + 1]), s2, cc), d0, d1);
+          S2 = add2(S2, pair(sc_ex2(d0), sc_ex2(d1)));
+        }
+      }
+    } else {
+      const bool mine_far = !(fabsf(c2) < DI_NEAR);
+      const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        if (u * 32 >= cv) break;
+        float f[VE];
+        sc_unpack<DT>(x[u], f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          S2 = add2(S2, pair(sc_ex2(mine_far ? (f[e] - base) * s : fmaf(f[e], s, -c2)), 0.f));
       }
     }
   }
@@ -262,7 +284,8 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
   {
     float a0, a1;
     unpair(S2, a0, a1);
-    st.S = (a0 + a1) * sc_ex2(mx == -INFINITY ? 0.f : (ref - mx) * s);  // from ref to mx
+    // to mx
+    st.S = (a0 + a1) * sc_ex2(mx == -INFINITY ? 0.f : fabsf(c2) < DI_NEAR ? -fmaf(mx, s, -c2) : (ref - mx) * s);
     if (!(mx < INFINITY) || !(xe < INFINITY)) wrong |= DI_NONFINITE;
   }
   sc_add(st, xe, s);
@@ -286,33 +309,37 @@ __global__ void __launch_bounds__(ST, ST == 64 ? SSMALL : SROWS * 256 / ST)
     }
     cluster_arrive();
     cluster_wait();
-    if (rank_c || warp) return;  // the first CTA has everything
-    join(sh.part, nc);
+    if (rank_c) return;  // the first CTA has everything
+    if (warp == WF) join(sh.part, nc);
   } else {
     __syncthreads();
-    if (warp) return;
-    join(sh.warp, SW);
+    if (warp == WF) join(sh.warp, EXTRA ? SW + 1 : SW);
   }
-  total = 0.0;
-#pragma unroll
-  for (int w = 0; w < SW; ++w) total += sh.total[w];
-  distill_finish(a, r, T, t, xt, wrong, st.m, st.S, sh.slots, total);
+  if (warp == WF) distill_finish(a, r, T, s, t, xt, wrong, st.m, st.S, sh.slots, sh.row);
+  if (EXTRA || K <= 32 || (!a.slot_lp && !a.slot_g)) {
+    if (warp != WF) return;
+    __syncwarp();
+    for (int k = lane; k < K && (a.slot_lp || a.slot_g); k += 32) distill_slot(a, r, k, sh.slots, sh.row);
+  } else {
+    __syncthreads();
+    for (int k = tid; k < K; k += ST) distill_slot(a, r, k, sh.slots, sh.row);
+  }
   // a later launch ends only after the one it started beside, so the last ends last
-  if (r0 && blockIdx.x == 0 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r0 && blockIdx.x == 0 && lane == 0 && warp == WF) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Rows [r0, r0 + rows), a row in nc CTAs of ST threads.
-template <int DT, int ST>
+template <int DT, int ST, bool EXTRA>
 int launch_distill(const DistillArgs& a, int r0, int rows, int nc, cudaStream_t st) {
   const bool more = r0 + rows < a.B;
   constexpr int VE = DT == SMP_F32 ? 4 : 8, CV = 32 << SLNU;
   const int seg = (a.V / VE + nc - 1) / nc;
   const int even = (seg + ST - 1) / ST * 32, cv = even < 32 ? 32 : even > CV ? CV : even;
   if ((long long)rows * nc > 0x7fffffffLL) return SMP_ERR_CAPACITY;
-  const auto kernel = a.bitmask ? distill_kernel<DT, ST, true> : distill_kernel<DT, ST, false>;
+  const auto kernel = a.bitmask ? distill_kernel<DT, ST, true, EXTRA> : distill_kernel<DT, ST, false, EXTRA>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * nc));
-  cfg.blockDim = dim3(ST);
+  cfg.blockDim = dim3(ST + (EXTRA ? 32 : 0));
   cfg.stream = st;
   cfg.dynamicSmemBytes = ST / 32 * DI_STAGES * cv * 16;
   if (!sc_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ST / 32 * DI_STAGES * CV * 16)))
@@ -333,22 +360,28 @@ int launch_distill(const DistillArgs& a, int r0, int rows, int nc, cudaStream_t 
 }
 
 // Short rows take CTAs of 2 or 4 warps.  Long ones take CTAs of 8, and the rows left when all
-// others fill the SMs a launch of their own, in clusters as large as still fit at once.
+// others fill the SMs a launch of their own, in clusters as large as still fit at once.  CTAs
+// that fill the SMs would all be at their slots at the same time, round after round: there
+// one more warp takes them while the others stream (4096 x 128256 bf16 with 32 slots 157 us,
+// 180 without it), unless they take it longer than the stream takes (912 x 128256: with 64
+// slots 42 and 46 us, with 192 62 and 54; 1824 x 20000: with 32 31 and 39, with 128 71 and
+// 52): 96 vectors of the row to a slot, or 32 slots at most.
 template <int DT>
 int distill_rows(const DistillArgs& a, cudaStream_t st) {
   const int sms = sc_sm_count();
   if (sms < 1) return SMP_ERR_CUDA;
   const int vectors = a.V / (DT == SMP_F32 ? 4 : 8);
-  if (vectors <= 64 * 8) return launch_distill<DT, 64>(a, 0, a.B, 1, st);
-  if (vectors <= 128 * 8) return launch_distill<DT, 128>(a, 0, a.B, 1, st);
+  if (vectors <= 64 * 8) return launch_distill<DT, 64, false>(a, 0, a.B, 1, st);
+  if (vectors <= 128 * 8) return launch_distill<DT, 128, false>(a, 0, a.B, 1, st);
   const int slots = SROWS * sms, done = a.B / slots * slots, rows = a.B - done;
   if (done) {
-    const int rc = launch_distill<DT, 256>(a, 0, done, 1, st);
+    const int rc = a.K <= 32 || vectors >= 96 * a.K ? launch_distill<DT, 256, true>(a, 0, done, 1, st)
+                                                    : launch_distill<DT, 256, false>(a, 0, done, 1, st);
     if (rc != SMP_OK || !rows) return rc;
   }
   int nc = 1;
   while (nc < SMAXC && (long long)rows * nc * 2 <= slots && vectors > nc * 256 * 8) nc *= 2;
-  return launch_distill<DT, 256>(a, done, rows, nc, st);
+  return launch_distill<DT, 256, false>(a, done, rows, nc, st);
 }
 
 }  // namespace
