@@ -6,8 +6,8 @@
 // keeps in shared memory
 //   touched  one bit a cell: in the history or biased;
 //   table    the touched cells, by open addressing: copies among the generated tokens,
-//            whether the token was seen, and its bias's slot (a token with several slots
-//            is marked, and its biases are then looked up in slot order);
+//            whether the token was seen, and its bias (a token with several slots is
+//            marked, and its biases are then looked up in slot order);
 //   count    for long histories, in place of their part of the table: a word for each cell.
 // Integer atomics only, so that results do not depend on the order of arrival.  Then the
 // segment streams from the logits to the result with its mask, and the few touched tokens
@@ -75,8 +75,8 @@ __device__ __forceinline__ int process_entry(int* keys, int size, int key, bool 
     if (++at == size) at = 0;
   }
 }
-// A touched token's result from its logit, its number and its bias's slot.
-__device__ __forceinline__ float process_token(const ProcessArgs& a, const ProcessRow& p, float v, uint32_t n, int place,
+// A touched token's result from its logit, its number and its only bias.
+__device__ __forceinline__ float process_token(const ProcessArgs& a, const ProcessRow& p, float v, uint32_t n, float only,
                                                int id, const int32_t* bias_ids, const float* bias) {
   if (v == -INFINITY) return v;
   v = process_penalty(p, v, n);
@@ -84,7 +84,7 @@ __device__ __forceinline__ float process_token(const ProcessArgs& a, const Proce
     for (int i = 0; i < a.NB; ++i)
       if (bias_ids[i] == id) v = process_bias(v, bias[i]);
   } else if (n & PBIAS) {
-    v = process_bias(v, bias[place]);
+    v = process_bias(v, only);
   }
   return v;
 }
@@ -112,13 +112,12 @@ __global__ void __launch_bounds__(PSPARSE, 2) process_sparse_kernel(const Proces
   extern __shared__ __align__(16) uint32_t words[];
   int* keys = reinterpret_cast<int*>(words);  // tokens; -1: none
   uint32_t* numbers = words + size;
-  int* places = reinterpret_cast<int*>(numbers + size);  // slots; -1: none; only with biases
+  float* biases = reinterpret_cast<float*>(numbers + size);  // of tokens with one; only with biases
   const int r = blockIdx.x, tid = threadIdx.x;
   raw* row = static_cast<raw*>(a.out) + (size_t)r * a.old;
   for (int i = tid; i < size; i += PSPARSE) {
     keys[i] = -1;
     numbers[i] = 0u;
-    if (a.NB) places[i] = -1;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t* history = a.history + (size_t)r * a.hld;
@@ -159,8 +158,8 @@ __global__ void __launch_bounds__(PSPARSE, 2) process_sparse_kernel(const Proces
     }
     if (id[k] >= 0) {
       const int at = process_entry(keys, size, id[k], true);
-      const bool several = atomicCAS(&places[at], -1, tid + k * PSPARSE) != -1;
-      atomicOr(&numbers[at], several ? PBIAS | PMULTI : PBIAS);
+      if (atomicOr(&numbers[at], PBIAS) & PBIAS) atomicOr(&numbers[at], PMULTI);
+      else biases[at] = b[k];
     }
   }
   __syncthreads();
@@ -168,8 +167,7 @@ __global__ void __launch_bounds__(PSPARSE, 2) process_sparse_kernel(const Proces
     const int j = keys[i];
     if (j < 0) continue;
     const uint32_t n = numbers[i];
-    const int place = a.NB ? places[i] : -1;
-    row[j] = TY::store(process_token(a, p, TY::value(row[j]), n, place, j, bias_ids, bias));
+    row[j] = TY::store(process_token(a, p, TY::value(row[j]), n, n & PBIAS ? biases[i] : 0.f, j, bias_ids, bias));
   }
 }
 
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
   uint32_t* count = touched + plan.bits;
   int* keys = reinterpret_cast<int*>(count + plan.counts);  // cells; -1: none
   uint32_t* numbers = reinterpret_cast<uint32_t*>(keys + plan.table);
-  int* places = reinterpret_cast<int*>(numbers + plan.table);  // slots; -1: none; only with biases
+  float* biases = reinterpret_cast<float*>(numbers + plan.table);  // of cells with one; only with biases
   // The launch gets ready under the end of the work before it on the stream: nothing of
   // a caller's is read or written before that is complete.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -224,7 +222,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
     // the first chunk of a row may start before it
     const int j0 = vb * VE - lead, k = (j0 >> 5) + lane;
     lo = k >= 0 && k < a.W ? bm[k] : ~0u;
-    hi = (j0 >> 5) + 32 < a.W ? bm[(j0 >> 5) + 32] : ~0u;
+    hi = (j0 & 31) && (j0 >> 5) + 32 < a.W ? bm[(j0 >> 5) + 32] : ~0u;
   };
   uint32_t mask_lo = ~0u, mask_hi = ~0u;  // of the next chunk
   if (MASK && v0 + warp * chunk < w1) mask_words(v0 + warp * chunk, mask_lo, mask_hi);
@@ -237,13 +235,17 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
   const int length = a.lengths ? a.lengths[r] : a.H, prompt = a.prompts ? a.prompts[r] : 0;
   // the first of the history and the biases, on their way with the parameters
   int early[PEARLY], bias_id = -1;
+  float first_bias = 0.f;
 #pragma unroll
   for (int k = 0; k < PEARLY; ++k) early[k] = !DENSE && tid + k * PT < a.H ? history[tid + k * PT] : -1;
   bool bad = !process_valid(p, length, prompt, a.H);
   for (int i = tid; i < a.NB; i += PT) {
     const int id = bias_ids[i];
     const float b = bias[i];
-    if (i == tid) bias_id = id;
+    if (i == tid) {
+      bias_id = id;
+      first_bias = b;
+    }
     if ((unsigned)id < (unsigned)a.V && !(b < INFINITY)) bad = true;
   }
   const bool any = a.H > 0 || a.NB > 0;
@@ -253,7 +255,6 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
     for (int i = tid; i < plan.table; i += PT) {
       keys[i] = -1;
       numbers[i] = 0u;
-      if (a.NB) places[i] = -1;
     }
     bad = __syncthreads_or(bad);
   } else {
@@ -314,9 +315,9 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
       const int id = i == tid ? bias_id : bias_ids[i], u = id - base;
       if ((unsigned)(id - j0) >= span) continue;
       const int at = process_entry(keys, plan.table, u, true);
-      const bool several = atomicCAS(&places[at], -1, i) != -1;
-      atomicOr(DENSE && a.H ? &count[u] : &numbers[at], PBIAS);
-      if (several) atomicOr(&numbers[at], PMULTI);
+      if (atomicOr(&numbers[at], PBIAS) & PBIAS) atomicOr(&numbers[at], PMULTI);
+      else biases[at] = i == tid ? first_bias : bias[i];
+      if (DENSE && a.H) atomicOr(&count[u], PBIAS);
       if (!(DENSE && a.H)) atomicOr(&touched[u >> 5], 1u << (u & 31));
     }
     __syncthreads();
@@ -334,13 +335,13 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
   auto changed = [&](float v, int u, int id) {
     const bool by_cell = DENSE && a.H > 0;
     uint32_t n = by_cell ? count[u] : 0u;
-    int place = -1;
+    float only = 0.f;
     if (!by_cell || (n & PBIAS)) {
       const int at = process_entry(keys, plan.table, u, false);
       n |= numbers[at];
-      if (a.NB) place = places[at];
+      if (n & PBIAS) only = biases[at];
     }
-    return process_token(a, p, v, n, place, id, bias_ids, bias);
+    return process_token(a, p, v, n, only, id, bias_ids, bias);
   };
   const bool look = any && !bad, masked = MASK && !bad;
   for (int vb = v0 + warp * chunk; vb < w1; vb += SW * chunk) {

@@ -7,7 +7,7 @@ import math
 import torch
 
 from .binding import _DTYPES, _check, load_library
-from .scoring import _F32, _I32, _bitmask, _current_device, _matrix, _need, _opt, _raw_stream, _width
+from .scoring import _F32, _I32, _bitmask, _current_device, _matrix, _need, _raw_stream, _width
 
 
 def process_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None, presence=None,
@@ -40,20 +40,23 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, repe
     dtype = logits.dtype if dtype is None else dtype
     if dtype is not logits.dtype and (dtype is not _F32 or in_place):
         raise ValueError(f"results of {logits.dtype} logits cannot be {dtype}" + (" in place" if in_place else ""))
-    H = hist = NB = ids = b = None
+    hist = ids = b = None
+    H = NB = 0
     if history is not None:
-        if history.dim() != 2 or history.shape[0] != B:
+        shape = history.shape
+        if len(shape) != 2 or shape[0] != B:
             raise ValueError("history must be [B, H]")
-        H = history.shape[1]
+        H = shape[1]
         hist = _need(history, "history", dev, _I32, B * H)
     elif lengths is not None or prompt_lengths is not None:
         raise ValueError("lengths and prompt_lengths need a history")
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias go together")
     if bias is not None:
-        if bias.dim() != 2 or bias.shape[0] != B or bias_ids.shape != bias.shape:
+        shape = bias.shape
+        if len(shape) != 2 or shape[0] != B or bias_ids.shape != shape:
             raise ValueError("bias_ids and bias must be [B, NB]")
-        NB = bias.shape[1]
+        NB = shape[1]
         ids, b = _need(bias_ids, "bias_ids", dev, _I32, B * NB), _need(bias, "bias", dev, _F32, B * NB)
     if out is None:
         status = torch.empty(B, dtype=_I32, device=logits.device)
@@ -66,17 +69,19 @@ def process_logits(logits, history=None, lengths=None, prompt_lengths=None, repe
         out = dict(logits=result, status=status)
     else:
         result = logits if in_place else out["logits"]
-        if result.dim() != 2 or result.shape[0] != B or result.shape[1] < V:
-            raise ValueError(f"out must be [{B}, at least {V}], got {list(result.shape)}")
         if in_place:
             out["logits"] = logits
-    to = _need(result, "out", dev, dtype, result.numel())
-    rc = L.smp_process_logits(logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, hist, H or 0, H or 0,
-                              _opt(lengths, "lengths", dev, _I32, B),
-                              _opt(prompt_lengths, "prompt_lengths", dev, _I32, B),
-                              _opt(repetition, "repetition", dev, _F32, B), _opt(presence, "presence", dev, _F32, B),
-                              _opt(frequency, "frequency", dev, _F32, B), ids, b, NB or 0,
-                              _bitmask(bitmask, dev, B, V), to, _DTYPES[dtype], result.shape[1],
+    shape = result.shape
+    if len(shape) != 2 or shape[0] != B or shape[1] < V:
+        raise ValueError(f"out must be [{B}, at least {V}], got {list(shape)}")
+    rc = L.smp_process_logits(logits.data_ptr(), _DTYPES[logits.dtype], B, V, ld, hist, H, H,
+                              None if lengths is None else _need(lengths, "lengths", dev, _I32, B),
+                              None if prompt_lengths is None else _need(prompt_lengths, "prompt_lengths", dev, _I32, B),
+                              None if repetition is None else _need(repetition, "repetition", dev, _F32, B),
+                              None if presence is None else _need(presence, "presence", dev, _F32, B),
+                              None if frequency is None else _need(frequency, "frequency", dev, _F32, B), ids, b, NB,
+                              None if bitmask is None else _bitmask(bitmask, dev, B, V),
+                              _need(result, "out", dev, dtype, B * shape[1]), _DTYPES[dtype], shape[1],
                               _need(out["status"], "status", dev, _I32, B), _raw_stream(dev))
     _check(rc, "smp_process_logits")
     return out
