@@ -29,7 +29,9 @@
  * kept set, for comparison) and smp_spec_verify (speculative-decoding
  * verification against the kept sets' probabilities); smp_token_logprobs,
  * smp_token_logprobs_grad and smp_head_logprobs (scoring of given tokens, for
- * training on them or reporting them); smp_set_kernel chooses between the two
+ * training on them or reporting them); smp_process_logits (penalties, biases and
+ * masks in one call); smp_distill_loss and smp_distill_loss_grad (a student's
+ * divergence from a teacher's top tokens); smp_set_kernel chooses between the two
  * sampler kernels; smp_set_wait_limit and smp_set_scoring_wait_limit bound the
  * device-side waits.
  *
@@ -428,8 +430,8 @@ int64_t smp_head_workspace(int N, int V);
  *               finite, a length outside [0, H], a prompt length outside [0,
  *               length], or a bias in a used slot that is NaN or +inf; the row
  *               then goes through unchanged, without its mask.
- * Logits that are NaN stay NaN, -inf stays -inf (a negative or NaN logit that is
- * masked becomes -inf).
+ * Logits that are NaN stay NaN, -inf stays -inf; what is masked becomes -inf,
+ * whatever it was.
  * Call status: SMP_ERR_INVALID_PARAM for NULL required pointers, B < 0, V < 1,
  * ld < V, out_ld < V, H < 0, history_ld < H, NB < 0, an out_dtype that is neither
  * dtype nor SMP_F32, or out == logits with another type or ld; SMP_ERR_CAPACITY

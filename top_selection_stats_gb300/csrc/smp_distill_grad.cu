@@ -44,18 +44,6 @@ __device__ __forceinline__ void distill_grad_pair(const DistillGradRow& q, float
   unpair(mul2(pair(sc_ex2(e0), sc_ex2(e1)), pair(q.D, q.D)), x0, x1);
 }
 
-// 16 bytes that start `off` bytes into p[0] (0: p[0] itself, and p[1] is not read).
-__device__ __forceinline__ uint4 vector_across(const uint4* p, int off) {
-  const uint4 a = p[0], b = off ? p[1] : a;
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t y[5];
-  const int k = off >> 2, bits = (off & 3) * 8;
-#pragma unroll
-  for (int i = 0; i < 5; ++i) y[i] = k == 0 ? w[i] : k == 1 ? w[i + 1] : k == 2 ? w[i + 2] : w[min(i + 3, 7)];
-  return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
-                    __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
-}
-
 // What the row's parameters come to: D = q.D 2^-shift with 2^shift in q.l2, and the
 // slots' scale, (g, g_lp) / T = (gm, glm) / Tm 2^e.
 struct DistillGradScale {

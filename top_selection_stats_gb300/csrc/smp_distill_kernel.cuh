@@ -10,6 +10,10 @@
 // cost more than the sums.  Their own logits are fetched one by one at the start,
 // under the first copies, and enter at the end (distill_finish).  A sum has no
 // second moment here, so -inf needs no clamp: 2^-inf is 0.
+//
+// Bound by HBM where rows fill the SMs: 4096 x 128256 bf16 with 32 slots 157 us, 6.7 TB/s (a
+// copy of as many bytes: 156); 1024 x 256000 f16 with 128: 90 us (78), 2.25 rounds of rows.
+// One row of 128256: 7.5 us, a launch and the chain of slots, stream, cluster and finish.
 #pragma once
 
 #include "smp_distill.cuh"
@@ -19,7 +23,7 @@ namespace smp {
 namespace {
 
 constexpr int DI_STAGES = 2;  // chunks a warp has in flight
-constexpr float DI_NEAR = 1.0e30f;
+constexpr float DI_NEAR = 1.0e30f;  // products x s whose differences cannot pass binary32
 
 struct DistillPart {
   float m, S;
@@ -163,9 +167,8 @@ __global__ void __launch_bounds__(ST + (EXTRA ? 32 : 0), ST == 64 ? SSMALL : SRO
     const bool raise = (top - ref) * s > SLAG;
     if (__any_sync(0xffffffffu, raise)) {
       if (raise) {
+        // from one reference to the other, as the sum is held
         const float e = sc_ex2(ref == -INFINITY ? SC_DMIN : (ref - top) * s);
-        // from one reference to the other, as the sum is held: 2^(c - (top s)) is exact to a
-        // rounding where the products are
         const float to = top * s;
         const bool near = fabsf(to) < DI_NEAR && fabsf(c2) < DI_NEAR;
         const float by = ref > -INFINITY && near ? sc_ex2(c2 - to) : e;

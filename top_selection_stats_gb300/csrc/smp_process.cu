@@ -14,6 +14,11 @@
 // of a vector are computed from its registers and written over it by the same thread, while
 // its line is in L2.  In place only vectors with something masked or touched are read, and
 // those without a legal token are written without being read.
+//
+// Bound by HBM where rows are long and many: 1024 x 256000 f16 to binary32 248 us, 6.4 TB/s
+// (a copy of as many bytes: 233).  Small calls are bound by the chain of a launch, parameters,
+// history, table and logits (1 x 128256 with 1000 entries 3.6 us), long histories by the
+// instructions that look through them in every CTA of the row.
 #include "smp_score_kernel.cuh"
 #include "smp_train.cuh"
 
@@ -87,18 +92,6 @@ __device__ __forceinline__ float process_token(const ProcessArgs& a, const Proce
     v = process_bias(v, only);
   }
   return v;
-}
-
-// 16 bytes that start `off` bytes into p[0] (0: p[0] itself, and p[1] is not read).
-__device__ __forceinline__ uint4 process_across(const uint4* p, int off) {
-  const uint4 a = p[0], b = off ? p[1] : a;
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t y[5];
-  const int k = off >> 2, bits = (off & 3) * 8;
-#pragma unroll
-  for (int i = 0; i < 5; ++i) y[i] = k == 0 ? w[i] : k == 1 ? w[i + 1] : k == 2 ? w[i + 2] : w[min(i + 3, 7)];
-  return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
-                    __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
 }
 
 enum { PR_COPY = 0, PR_ACROSS = 1, PR_IN_PLACE = 2 };
@@ -211,7 +204,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
 #pragma unroll
     for (int u = 0; u < PU; ++u) {
       const int v = vb + u * 32 + lane;
-      if (u < each && v >= w0 && v < w1) x[u] = HOW == PR_ACROSS ? process_across(src + v, off) : __ldcs(src + v);
+      if (u < each && v >= w0 && v < w1) x[u] = HOW == PR_ACROSS ? vector_across(src + v, off) : __ldcs(src + v);
     }
   };
   if (HOW != PR_IN_PLACE) load(v0 + warp * chunk);
@@ -442,8 +435,14 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
 }
 
 // Histories and biases of up to PSHORT entries go into a table, and a segment is as long
-// as the batch allows: rounds of CTAs times what each has to do, its look through the
-// history counted as PSETUP cells.  Longer ones are counted by cell in segments of PDENSE.
+// as the batch allows: rounds of CTAs times what each has to do, its set-up counted as
+// PSETUP cells (in place, where a cell is less work, as twice that).  1024 x 256000 f16 to
+// binary32 with 512 entries: 248 us with PSETUP 1024 or 2048, 273 with 4096; 512 x 151936
+// masked in place: 42, 33 and 30.  Longer ones are counted by cell, by CTAs of 1024 threads, as
+// nearly all the work is to look through the history: 64 x 32000 with 4096 entries 16 us, 18
+// with 512 threads; 16 x 50001 with 65536 entries 12.7, and 41 where the CTAs of a row share
+// the entries and count into each other's shared memory.  Up to 2048 entries the table is
+// faster: 128 x 128256 with 1500 entries 18 us, 36 counted by cell.
 template <int DT, int OT, int HOW>
 int launch_process(const ProcessArgs& a, int sms, cudaStream_t st) {
   constexpr int VE = DT == SMP_F32 ? 4 : 8;

@@ -54,6 +54,18 @@ struct DistillGradArgs {
   int B, V, W, K;
 };
 
+// 16 bytes that start `off` bytes into p[0] (0: p[0] itself, and p[1] is not read).
+__device__ __forceinline__ uint4 vector_across(const uint4* p, int off) {
+  const uint4 a = p[0], b = off ? p[1] : a;
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t y[5];
+  const int k = off >> 2, bits = (off & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) y[i] = k == 0 ? w[i] : k == 1 ? w[i + 1] : k == 2 ? w[i + 2] : w[min(i + 3, 7)];
+  return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
+                    __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
+}
+
 int process_enqueue(const ProcessArgs& a, int dtype, int out_dtype, cudaStream_t st);
 int distill_f32(const DistillArgs& a, cudaStream_t st);
 int distill_bf16(const DistillArgs& a, cudaStream_t st);
