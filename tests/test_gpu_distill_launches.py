@@ -32,12 +32,14 @@ def test_rows_that_fill_the_sms(kind, V, K, B):
     small = G.make(6, V, K, "bf16", V + K, kind, masked=K == 33, unused=0.1)
     if K > 32:
         small["ids"][5, K - 1] = small["ids"][5, 0] = 7  # the same id twice, in two warps' slots
+    far = torch.tensor([-(1 << 31), (1 << 31) - 1, 1 << 30, V, -2], dtype=torch.int32, device="cuda")
+    small["ids"][4, :min(K, 5)] = far[:min(K, 5)]
     G.check_forward(small)
     c, order = repeated(small, B)
     got, want = G.run(c), G.run(small)
     ref = G.reference(small)
     assert list(got["status"].cpu()) == [ref[i]["status"] for i in order.tolist()]
-    assert K <= 32 or ref[5]["status"] == 3
+    assert ref[4]["status"] == 3 and (K <= 32 or ref[5]["status"] == 3)
     T = small["temperature"].cpu().numpy()
     for r, i in enumerate(order.tolist()):
         if ref[i]["status"] != 0 or r % 37 and r < B - 12:

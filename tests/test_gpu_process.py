@@ -186,6 +186,19 @@ def test_extreme_values(dtype, in_place):
     check(c, dtype, in_place=in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("H", [40, 3000])
+def test_ids_far_outside(H, in_place):
+    """Entries and biases at the ends of int32 are padding."""
+    c = make(3, 30001, H, 40, "bf16", 9, shift=3, masked=H == 40)
+    far = torch.tensor([-(1 << 31), (1 << 31) - 1, -(1 << 31) + 30000, 1 << 30, 30001, -1], dtype=torch.int32, device="cuda")
+    c["history"][:, 3:9] = far
+    c["bias_ids"][:, 3:9] = far
+    check(c, "bf16", in_place=in_place)
+    del c["bitmask"]
+    check(c, "bf16", in_place=in_place)
+
+
 def test_masks_that_leave_nothing():
     c = make(4, 3000, 10, 3, "bf16", 1, masked=True)
     c["bitmask"][1] = 0

@@ -150,9 +150,11 @@ __global__ void __launch_bounds__(DGT, DGCTAS) distill_grad_kernel(const Distill
   if (!none) {
     bool taken = false;
     for (int k0 = 0; k0 < a.K; k0 += 32) {
-      const int k = k0 + lane, id = k < a.K ? a.ids[(size_t)r * a.K + k] : -1, v = (id + lead) / VE;
-      taken |= id >= 0 && id == target;
-      const bool in_row = id >= 0 && id < a.V, end = v < f0 || v >= f1;
+      const int k = k0 + lane, given = k < a.K ? a.ids[(size_t)r * a.K + k] : -1;
+      const bool in_row = given >= 0 && given < a.V;
+      const int id = in_row ? given : 0, v = (id + lead) / VE;
+      taken |= in_row && id == target;
+      const bool end = v < f0 || v >= f1;
       const bool mine = in_row && (end ? c == 0 && warp == 0 : v >= v0 && v < v1 && (v - v0) % DGT / 32 == warp);
       const uint32_t which = __ballot_sync(0xffffffffu, mine);
       if (mine) {

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(ST + (EXTRA ? 32 : 0), ST == 64 ? SSMALL : SRO
     raw* values = reinterpret_cast<raw*>(stage);
     bool wrote = false;
     for (int k = lane; k < K; k += 32) {
-      const unsigned d = (unsigned)((EXTRA ? a.ids[(size_t)r * K + k] : sh.slots.ids[k]) - first);
+      const unsigned d = (unsigned)(EXTRA ? a.ids[(size_t)r * K + k] : sh.slots.ids[k]) - (unsigned)first;
       if (d < (unsigned)(cv * VE)) {
         if constexpr (DT == SMP_F32) values[d] = -INFINITY;
         else values[d] = (raw)(WD::NONE & 0xffffu);

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
           }
 #pragma unroll
           for (int k = 0; k < PBATCH; ++k) {
-            if ((unsigned)(t[k] - j0) < span) {
+            if ((unsigned)t[k] - (unsigned)j0 < span) {
               if (generated) atomicAdd(&count[t[k] - base], 1u);
               else atomicOr(&count[t[k] - base], PSEEN);
             }
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
       scan(prompt, length, true);
     } else {
       auto seen = [&](int t, int i) {  // entry i of the history
-        if (i >= length || (unsigned)(t - j0) >= span) return;
+        if (i >= length || (unsigned)t - (unsigned)j0 >= span) return;
         const int u = t - base;
         uint32_t* n = &numbers[process_entry(keys, plan.table, u, true)];
         if (i < prompt) atomicOr(n, PSEEN);
@@ -305,8 +305,9 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
       }
     }
     for (int i = tid; i < a.NB; i += PT) {
-      const int id = i == tid ? bias_id : bias_ids[i], u = id - base;
-      if ((unsigned)(id - j0) >= span) continue;
+      const int id = i == tid ? bias_id : bias_ids[i];
+      if ((unsigned)id - (unsigned)j0 >= span) continue;
+      const int u = id - base;
       const int at = process_entry(keys, plan.table, u, true);
       if (atomicOr(&numbers[at], PBIAS) & PBIAS) atomicOr(&numbers[at], PMULTI);
       else biases[at] = i == tid ? first_bias : bias[i];
