@@ -33,6 +33,7 @@ class DistillLoss(torch.autograd.Function):
         return out["loss"], out["logprobs"]
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss, grad_logprobs):
         logits, ids, targets, temperature, slot_logprobs, slot_grads, stats, logprobs = ctx.saved_tensors
         grad = distill_loss_grad(logits, ids, slot_logprobs, slot_grads, stats, grad_loss.contiguous(), targets=targets,

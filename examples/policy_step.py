@@ -31,6 +31,7 @@ class TokenLogprobs(torch.autograd.Function):
         return out["logprobs"], out["entropy"]
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_logprobs, grad_entropy):
         logits, targets, temperature, stats, entropy = ctx.saved_tensors
         grad = token_logprobs_grad(logits, targets, stats, grad_logprobs.contiguous(), entropy=entropy,
