@@ -23,7 +23,10 @@ namespace smp {
 namespace {
 
 constexpr int DI_STAGES = 2;  // chunks a warp has in flight
-constexpr float DI_NEAR = 1.0e30f;  // products x s whose differences cannot pass binary32
+// Products x s below this are rounded by half a unit at most, so that a sum relative to a
+// rounded one has a value next to its reference between 2^-1/2 and 2^1/2 (at 2^34 it would be
+// off by up to 2^9, past what 2^x can hold).
+constexpr float DI_NEAR = 0x1p24f;
 
 struct DistillPart {
   float m, S;
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(ST + (EXTRA ? 32 : 0), ST == 64 ? SSMALL : SRO
 
   // The lane's sum is of 2^(x s - c): one fused operation a value, rounded once whatever c
   // is.  c follows its largest value mx only when that has left it by a factor of 2^SLAG.
-  // Where x s would pass binary32 (far), the sum is of 2^((x - ref) s).
+  // Where c would be rounded by more than half a unit (far), the sum is of 2^((x - ref) s).
   float ref = -INFINITY, c2 = 0.f, mx = -INFINITY;
   bool far = false;  // of some lane of the warp
   f32x2 S2 = pair(0.f, 0.f);
@@ -167,11 +170,12 @@ __global__ void __launch_bounds__(ST + (EXTRA ? 32 : 0), ST == 64 ? SSMALL : SRO
     const bool raise = (top - ref) * s > SLAG;
     if (__any_sync(0xffffffffu, raise)) {
       if (raise) {
-        // from one reference to the other, as the sum is held
-        const float e = sc_ex2(ref == -INFINITY ? SC_DMIN : (ref - top) * s);
+        // from what the sum is relative to (c, or ref s where that is far) to the same of top,
+        // rounded once
         const float to = top * s;
-        const bool near = fabsf(to) < DI_NEAR && fabsf(c2) < DI_NEAR;
-        const float by = ref > -INFINITY && near ? sc_ex2(c2 - to) : e;
+        const bool was = fabsf(c2) < DI_NEAR, is = fabsf(to) < DI_NEAR;
+        const float e = fmaf((was ? 0.f : ref) - (is ? 0.f : top), s, (was ? c2 : 0.f) - (is ? to : 0.f));
+        const float by = ref == -INFINITY ? 0.f : sc_ex2(e);
         S2 = mul2(S2, pair(by, by));
         ref = top;
         c2 = to;
