@@ -435,6 +435,9 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
   }
 }
 
+// Entries of a table for as many tokens.
+constexpr int process_table(int held) { return held + held / 2 + 8; }
+
 // Histories and biases of up to PSHORT entries go into a table, and a segment is as long
 // as the batch allows: rounds of CTAs times what each has to do, its set-up counted as
 // PSETUP cells (in place, where a cell is less work, as twice that).  1024 x 256000 f16 to
@@ -472,7 +475,7 @@ int launch_process(const ProcessArgs& a, int sms, cudaStream_t st) {
   plan.bits = (words + 3) & ~3;
   plan.counts = dense && a.H ? plan.seg * VE : 0;
   const int held = (dense && a.H ? 0 : a.H) + a.NB;
-  plan.table = held ? held + held / 2 + 8 : 0;
+  plan.table = held ? process_table(held) : 0;
   if ((long long)a.B * plan.nc > 0x7fffffffLL) return SMP_ERR_CAPACITY;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * plan.nc));
@@ -486,21 +489,26 @@ int launch_process(const ProcessArgs& a, int sms, cudaStream_t st) {
   cfg.numAttrs = 1;
   const auto kernel = dense ? (a.bitmask ? process_kernel<DT, OT, HOW, true, PLARGE> : process_kernel<DT, OT, HOW, false, PLARGE>)
                             : (a.bitmask ? process_kernel<DT, OT, HOW, true, PSMALL> : process_kernel<DT, OT, HOW, false, PSMALL>);
+  // The limit is the kernel's, for all threads of the process: always the most that a plan may
+  // have, as a call with less could set it between another's setting and its launch.
+  constexpr int by_cell = (PDENSE / 32 + PDENSE + 3 * process_table(PR_MAX_NB)) * 4;
+  constexpr int by_table = (PMOST / 32 + 3 * process_table(PSHORT)) * 4;
+  static_assert(by_cell <= 227 * 1024 && by_table <= 227 * 1024, "every plan fits an SM");
   if (cfg.dynamicSmemBytes > 48 * 1024 &&
-      !sc_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes)))
+      !sc_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense ? by_cell : by_table)))
     return SMP_ERR_CUDA;
   return sc_ok(cudaLaunchKernelEx(&cfg, kernel, a, plan)) ? SMP_OK : SMP_ERR_CUDA;
 }
 
 template <int DT>
 int launch_sparse(const ProcessArgs& a, cudaStream_t st) {
-  const int held = a.H + a.NB, size = held + held / 2 + 8;
+  const int size = process_table(a.H + a.NB);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.B);
   cfg.blockDim = dim3(PSPARSE);
   cfg.stream = st;
   cfg.dynamicSmemBytes = (size_t)size * (a.NB ? 3 : 2) * 4;
-  static_assert((PSHORT + PSHORT / 2 + 8) * 12 <= 48 * 1024, "the table needs no opt-in");
+  static_assert(process_table(PSHORT) * 12 <= 48 * 1024, "the table needs no opt-in");
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
