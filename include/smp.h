@@ -460,9 +460,10 @@ int smp_process_logits(const void* logits, smp_dtype dtype, int B, int V, int64_
  * (the first two: all other tokens are one class, and `teacher` holds log
  * probabilities; in the third it holds logits, at temperature 1, and the rest of
  * the teacher's distribution is left out).  When no legal token lies outside the
- * slots, the terms with r and s are 0.  Terms with weight 0 are 0; a slot of
- * weight > 0 whose other probability is 0 makes the loss +inf, and such a row has
- * no gradient of its loss.
+ * slots, the terms with r and s are 0.  Terms with weight 0 (a logarithm below
+ * -745.13, the least of binary64) are 0; a slot of weight > 0 whose other
+ * probability is 0 makes the loss +inf, whatever the slots' order, and such a row
+ * has no gradient of its loss.
  *   teacher_ids : DEVICE int32 [B][K], 1 <= K <= 256: token ids, -1 for an unused
  *                 slot.  A row without a used slot has loss 0 and no gradient.
  *   teacher     : DEVICE float [B][K]; -inf: probability 0.

@@ -21,7 +21,9 @@
 namespace smp {
 namespace {
 
-enum { DI_INVALID = 1, DI_NONFINITE = 2, DI_LATE = 4, DI_INFINITE = 8 };  // the last: an infinite loss
+enum { DI_INVALID = 1, DI_NONFINITE = 2, DI_LATE = 4 };
+// A slot's weight is 0 when its logarithm is below this, the least that binary64 has.
+constexpr float DI_LEAST_LOG = -745.1332f;
 
 __device__ __forceinline__ float di_sum(float v) {
 #pragma unroll
@@ -40,8 +42,11 @@ __device__ __forceinline__ float di_max(float v) {
 //   mass = sum w, teach = sum e, and cross, the mean of (y - d) / 2 under e (forward, truncated)
 //   or of (d - y) / 2 under w (reverse): halves, as a mean of values at the end of binary32
 //   may round past it.
+// Terms that are infinite unless their weight in the row is 0 are kept apart, as that is not
+// known here: lost is the largest logarithm, relative to m or top, of the weight of a slot that
+// the other side does not have, over the largest weight of one whose d has passed binary32.
 struct SlotPart {
-  float m, mass, top, teach, cross;
+  float m, mass, top, teach, cross, lost, over;
   int wrong;
   double total;  // sum e in binary64 (not truncated)
 };
@@ -83,17 +88,24 @@ __device__ __forceinline__ void distill_slots(const DistillArgs& a, Slots& slots
   }
   p.mass = di_sum(w);
   p.teach = di_sum(e);
-  // a term of weight 0 is 0; one whose other probability is 0 is infinite
   const float weight = reverse ? w : e;
   float cross = 0.f;
-  if (weight > 0.f) {
+  p.lost = -INFINITY;
+  p.over = 0.f;
+  if (reverse ? legal && !taught : taught && !legal) {
+    p.lost = reverse ? d : y;
+  } else if (weight > 0.f) {
     cross = __fdiv_rn(weight, reverse ? p.mass : p.teach) * (reverse ? 0.5f * d - 0.5f * y : 0.5f * y - 0.5f * d);
     if (!(cross < INFINITY)) {
-      p.wrong |= DI_INFINITE;
+      p.over = weight;
       cross = 0.f;
     }
   }
   p.cross = di_sum(cross);
+  if (__any_sync(0xffffffffu, p.lost > -INFINITY || p.over > 0.f)) {
+    p.lost = di_max(p.lost);
+    p.over = di_max(p.over);
+  }
   p.wrong = __reduce_or_sync(0xffffffffu, p.wrong);
   slots.x[k0 + lane] = x;
   slots.d[k0 + lane] = d;
@@ -116,7 +128,7 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
                                                float rest_m, float rest_S, const Slots& slots, RowResult& o) {
   const int lane = threadIdx.x & 31, parts = (a.K + 31) / 32;
   const bool reverse = a.kind == SMP_DISTILL_REVERSE, truncated = a.kind == SMP_DISTILL_TRUNCATED;
-  SlotPart p{-INFINITY, 0.f, truncated ? -INFINITY : 0.f, 0.f, 0.f, 0, 0.0};
+  SlotPart p{-INFINITY, 0.f, truncated ? -INFINITY : 0.f, 0.f, 0.f, -INFINITY, 0.f, 0, 0.0};
   if (lane < parts) p = slots.part[lane];
   wrong |= p.wrong;
   // the student: lane `parts` has what is outside the slots
@@ -152,9 +164,11 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
   const bool ok = status == SMP_OK;
   // the slots' part of the loss
   float loss = 0.f;
+  bool infinite = false;  // a slot of weight above 0 that the other side does not have
   if (lane < parts) {
-    const float q = reverse ? expf(shift) * p.mass : scale * p.teach;  // the part's weight
+    const float by = reverse ? expf(shift) : scale, q = by * (reverse ? p.mass : p.teach);  // the part's weight
     if (q > 0.f) loss = q * (p.cross + 0.5f * (reverse ? shift : p.m > -INFINITY ? taught - shift : 0.f));
+    infinite = p.lost + (reverse ? shift : taught) >= DI_LEAST_LOG || by * p.over > 0.f;
   }
   loss = di_sum(loss);
   loss = loss > 0x1p127f && loss < 0x1.00001p127f ? 0x1.fffffep127f : 2.f * loss;
@@ -163,7 +177,7 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
     if (reverse) loss += mass > 0.f ? mass * (log_s - log_r) : 0.f;
     else loss += rest * (log_r - log_s);
   }
-  if (wrong & DI_INFINITE) loss = INFINITY;
+  if (__any_sync(0xffffffffu, infinite)) loss = INFINITY;
   const bool finite = fabsf(loss) < INFINITY;
   float A = 0.f;
   if (finite) {
