@@ -73,7 +73,9 @@ __device__ __forceinline__ void distill_slots(const DistillArgs& a, Slots& slots
   p.m = di_max(x);
   p.top = truncated ? di_max(v) : 0.f;
   const bool legal = x > -INFINITY, taught = v > -INFINITY;
-  const float w = legal ? sc_ex2((x - p.m) * s) : 0.f;
+  float w = legal ? sc_ex2((x - p.m) * s) : 0.f;
+  // 2^x flushes results below 2^-126, which a teacher's lowest finite values weigh up
+  if (reverse && legal && w == 0.f) w = __fmul_rn(sc_ex2((x - p.m) * s + 64.f), 0x1p-64f);
   const float d = legal ? __fdiv_rn(x - p.m, T) : -INFINITY;
   const float y = !taught ? -INFINITY : truncated ? __fdiv_rn(v - p.top, T) : v;
   float e = 0.f;
