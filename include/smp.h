@@ -498,8 +498,10 @@ int smp_distill_loss(const void* logits, smp_dtype dtype, int B, int V, int64_t 
 /* Gradient of smp_distill_loss' loss and logprobs with respect to the logits, for
  * a training loss with d / d loss[r] = grad_loss[r] and d / d logprobs[r] =
  * grad_logprobs[r], computed in binary32 and rounded once to `dtype`; 0 for tokens
- * that are not legal and in rows that failed.  grad_logprobs counts nothing in a
- * row without a target or with one that is not legal.
+ * that are not legal and in rows that failed, also where an incoming gradient is
+ * not finite (legal tokens of its row then get values that are not either).
+ * grad_logprobs counts nothing in a row without a target or with one that is not
+ * legal.
  *   logits, bitmask, temperature, teacher_ids, K, targets: as given to the forward
  *                   call (of any kind).
  *   slot_logprobs, slot_grads, stats, logprobs: the forward call's; slot_logprobs,

@@ -85,6 +85,13 @@ __device__ __forceinline__ DistillGradScale distill_grad_scale(const DistillGrad
   if (!(i.T > 0x1p-30f && i.T < 0x1p20f && size > 0x1p-60f && size < 0x1p40f && fabsf(i.A) < 0x1p40f)) o = distill_grad_far(i);
   o.q.m = i.m;
   o.q.s = sc_scale(i.T);
+  if (!(fabsf(o.q.D) < INFINITY)) {
+    // an incoming gradient that is not finite: 2^x is infinite for a finite logit and 0 for
+    // -inf, so that it is for legal tokens alone (0 times infinity is NaN)
+    o.q.D = o.q.D == INFINITY ? 1.f : o.q.D == -INFINITY ? -1.f : 0.f;
+    o.q.s = 0x1p-100f;
+    o.q.l2 = -0x1p100f;
+  }
   if (i.m == -INFINITY) o.q.m = o.q.l2 = o.q.D = 0.f;  // every legal token has a slot
   return o;
 }
@@ -160,6 +167,8 @@ __global__ void __launch_bounds__(DGT, DGCTAS) distill_grad_kernel(const Distill
       if (mine) {
         float y = sc.gm * a.slot_g[(size_t)r * a.K + k];
         if (sc.glm != 0.f) y += (id == target ? sc.glm : 0.f) - sc.glm * expf(a.slot_lp[(size_t)r * a.K + k]);
+        // 0 times infinity at a token that is not legal
+        if (!(fabsf(y) < INFINITY) && !((!MASK || ((bm[id >> 5] >> (id & 31)) & 1u)) && TY::value(row[id]) > -INFINITY)) y = 0.f;
         list[slots + __popc(which & ((1u << lane) - 1))] = make_int2(id, __float_as_int(ldexpf(y / sc.Tm, sc.e)));
       }
       slots += __popc(which);
