@@ -57,7 +57,13 @@ __device__ __forceinline__ float process_penalty(const ProcessRow& p, float v, u
   if (n & (PSEEN | PCOUNT)) {
     v = v > 0.f ? __fdiv_rn(v, p.theta) : __fmul_rn(v, p.theta);
     const float copies = (float)(n & PCOUNT);
-    v = __fsub_rn(v, __fadd_rn(__fmul_rn(p.frequency, copies), copies > 0.f ? p.presence : 0.f));
+    const float presence = copies > 0.f ? p.presence : 0.f, take = __fadd_rn(__fmul_rn(p.frequency, copies), presence);
+    if (fabsf(take) < INFINITY) {
+      v = __fsub_rn(v, take);
+    } else {  // past binary32, of numbers that are not: the same steps, 2^26 times smaller
+      constexpr float c = 0x1p-26f;
+      v = __fmul_rn(__fsub_rn(v * c, __fadd_rn(__fmul_rn(p.frequency * c, copies), presence * c)), 1.f / c);
+    }
   }
   return v;
 }
