@@ -112,6 +112,14 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
     const float lp = (xt - m) / T - L, p = expf(lp);
     q.at = (gs - (p > 0.f ? p * (gs + (a.g_ent ? hs * (lp + H) : 0.f)) : 0.f)) / st * (small ? 0x1p-24f : 0x1p63f);
   }
+  if (!(fabsf(q.c0) < INFINITY && fabsf(q.c1) < INFINITY)) {
+    // an incoming gradient that is not finite: 2^x is infinite for a finite logit (d is -255 at
+    // least) and 0 for -inf, so that legal tokens alone are not finite (0 times infinity is NaN)
+    q.c0 = q.c0 == INFINITY ? 1.f : q.c0 == -INFINITY ? -1.f : 0.f;
+    q.c1 = 0.f;
+    q.s = 0x1p-120f;
+    q.l2 = -5000.f;
+  }
 
   // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(raw));
