@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
   q.t = g != 0.f ? t : -1;
   const bool zero = !live || (g == 0.f && gh == 0.f);
   // with these the factors are in range (H - L is at most 17): no wait for the quotients
-  const float size = fmaxf(fabsf(g), fabsf(gh));
+  const float size = fabsf(g) + fabsf(gh);  // NaN is far too
   bool far = !zero && !(T > 0x1p-60f && T < 0x1p20f && size > 0x1p-70f && size < 0x1p60f);
   float most;
   if (far) {
@@ -111,14 +111,12 @@ __global__ void __launch_bounds__(GT) grad_kernel(const GradArgs a, const int nc
     q.l2 = L / SC_LN2 + (small ? 24.f : -63.f);
     const float lp = (xt - m) / T - L, p = expf(lp);
     q.at = (gs - (p > 0.f ? p * (gs + (a.g_ent ? hs * (lp + H) : 0.f)) : 0.f)) / st * (small ? 0x1p-24f : 0x1p63f);
-  }
-  if (!(fabsf(q.c0) < INFINITY && fabsf(q.c1) < INFINITY)) {
-    // an incoming gradient that is not finite: 2^x is infinite for a finite logit (d is -255 at
-    // least) and 0 for -inf, so that legal tokens alone are not finite (0 times infinity is NaN)
-    q.c0 = q.c0 == INFINITY ? 1.f : q.c0 == -INFINITY ? -1.f : 0.f;
-    q.c1 = 0.f;
-    q.s = 0x1p-120f;
-    q.l2 = -5000.f;
+    if (!(q.c0 == q.c0 && q.c1 == q.c1)) {
+      // NaN came in: infinity times 0 for tokens that have a probability, 0 times 0 for those
+      // that are not legal (d = SC_DMIN or -inf)
+      q.c0 = q.c1 = 0.f;
+      q.l2 = 0.5f * SC_DMIN;
+    }
   }
 
   // Vectors are aligned in memory: vector v has elements v VE - lead + [0, VE).
