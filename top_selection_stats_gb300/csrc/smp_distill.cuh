@@ -21,7 +21,7 @@
 namespace smp {
 namespace {
 
-enum { DI_INVALID = 1, DI_NONFINITE = 2, DI_LATE = 4 };
+enum { DI_INVALID = 1, DI_NONFINITE = 2, DI_LATE = 4, DI_APART = 8 };  // the last: a slot with lost or over
 // A slot's weight is 0 when its logarithm is below this, the least that binary64 has.
 constexpr float DI_LEAST_LOG = -745.1332f;
 
@@ -95,20 +95,22 @@ __device__ __forceinline__ void distill_slots(const DistillArgs& a, Slots& slots
   p.lost = -INFINITY;
   p.over = 0.f;
   if (reverse ? legal && !taught : taught && !legal) {
+    p.wrong |= DI_APART;
     p.lost = reverse ? d : y;
   } else if (weight > 0.f) {
     cross = __fdiv_rn(weight, reverse ? p.mass : p.teach) * (reverse ? 0.5f * d - 0.5f * y : 0.5f * y - 0.5f * d);
     if (!(cross < INFINITY)) {
+      p.wrong |= DI_APART;
       p.over = weight;
       cross = 0.f;
     }
   }
   p.cross = di_sum(cross);
-  if (__any_sync(0xffffffffu, p.lost > -INFINITY || p.over > 0.f)) {
+  p.wrong = __reduce_or_sync(0xffffffffu, p.wrong);
+  if (p.wrong & DI_APART) {
     p.lost = di_max(p.lost);
     p.over = di_max(p.over);
   }
-  p.wrong = __reduce_or_sync(0xffffffffu, p.wrong);
   slots.x[k0 + lane] = x;
   slots.d[k0 + lane] = d;
   slots.y[k0 + lane] = y;
@@ -166,11 +168,10 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
   const bool ok = status == SMP_OK;
   // the slots' part of the loss
   float loss = 0.f;
-  bool infinite = false;  // a slot of weight above 0 that the other side does not have
+  const float by = reverse ? expf(shift) : scale;
   if (lane < parts) {
-    const float by = reverse ? expf(shift) : scale, q = by * (reverse ? p.mass : p.teach);  // the part's weight
+    const float q = by * (reverse ? p.mass : p.teach);  // the part's weight
     if (q > 0.f) loss = q * (p.cross + 0.5f * (reverse ? shift : p.m > -INFINITY ? taught - shift : 0.f));
-    infinite = p.lost + (reverse ? shift : taught) >= DI_LEAST_LOG || by * p.over > 0.f;
   }
   loss = di_sum(loss);
   loss = loss > 0x1p127f && loss < 0x1.00001p127f ? 0x1.fffffep127f : 2.f * loss;
@@ -179,7 +180,10 @@ __device__ __forceinline__ void distill_finish(const DistillArgs& a, int r, floa
     if (reverse) loss += mass > 0.f ? mass * (log_s - log_r) : 0.f;
     else loss += rest * (log_r - log_s);
   }
-  if (__any_sync(0xffffffffu, infinite)) loss = INFINITY;
+  if (wrong & DI_APART) {  // of some part; infinite with a weight above 0
+    const bool counts = lane < parts && (p.lost + (reverse ? shift : taught) >= DI_LEAST_LOG || by * p.over > 0.f);
+    if (__any_sync(0xffffffffu, counts)) loss = INFINITY;
+  }
   const bool finite = fabsf(loss) < INFINITY;
   float A = 0.f;
   if (finite) {

@@ -57,6 +57,23 @@ struct DistillGradIn {
 // Any values: mantissas and powers apart.
 __device__ __noinline__ DistillGradScale distill_grad_far(const DistillGradIn i) {
   DistillGradScale o;
+  o.q.m = i.m;
+  if (!(fabsf(i.g) + fabsf(i.gl) < INFINITY)) {
+    // An incoming gradient that is not finite: results that are not, at legal tokens alone.
+    // Outside the slots 2^x is infinite for a finite logit and 0 for -inf, and D is 1, -1 or (NaN)
+    // 0; a slot's value is 2^300 times what a sign comes to, 0 at a token without probability.
+    const float D = i.g * i.A - i.gl * i.mass;
+    auto sign = [](float v) { return fabsf(v) < INFINITY ? 0.f : v < 0.f ? -1.f : 1.f; };
+    o.gm = sign(i.g);
+    o.glm = sign(i.gl);
+    o.Tm = 1.f;
+    o.e = 300;
+    o.q.D = D == INFINITY ? 1.f : D == -INFINITY ? -1.f : 0.f;
+    o.q.s = 0x1p-100f;
+    o.q.l2 = -0x1p100f;
+    return o;
+  }
+  o.q.s = sc_scale(i.T);
   int ge, le, Te, De;
   frexpf(i.g, &ge);
   frexpf(i.gl, &le);
@@ -74,7 +91,7 @@ __device__ __noinline__ DistillGradScale distill_grad_far(const DistillGradIn i)
 }
 // Values of ordinary size: every product and quotient is in range by itself.
 __device__ __forceinline__ DistillGradScale distill_grad_scale(const DistillGradIn& i) {
-  const float size = fmaxf(fabsf(i.g), fabsf(i.gl));
+  const float size = fabsf(i.g) + fabsf(i.gl);  // NaN is far too
   DistillGradScale o;
   o.gm = i.g;
   o.glm = i.gl;
@@ -82,16 +99,9 @@ __device__ __forceinline__ DistillGradScale distill_grad_scale(const DistillGrad
   o.e = 0;
   o.q.D = (i.g * i.A - i.gl * i.mass) / i.T * 0x1p-24f;
   o.q.l2 = i.L / SC_LN2 - 24.f;
-  if (!(i.T > 0x1p-30f && i.T < 0x1p20f && size > 0x1p-60f && size < 0x1p40f && fabsf(i.A) < 0x1p40f)) o = distill_grad_far(i);
   o.q.m = i.m;
   o.q.s = sc_scale(i.T);
-  if (!(fabsf(o.q.D) < INFINITY)) {
-    // an incoming gradient that is not finite: 2^x is infinite for a finite logit and 0 for
-    // -inf, so that it is for legal tokens alone (0 times infinity is NaN)
-    o.q.D = o.q.D == INFINITY ? 1.f : o.q.D == -INFINITY ? -1.f : 0.f;
-    o.q.s = 0x1p-100f;
-    o.q.l2 = -0x1p100f;
-  }
+  if (!(i.T > 0x1p-30f && i.T < 0x1p20f && size > 0x1p-60f && size < 0x1p40f && fabsf(i.A) < 0x1p40f)) o = distill_grad_far(i);
   if (i.m == -INFINITY) o.q.m = o.q.l2 = o.q.D = 0.f;  // every legal token has a slot
   return o;
 }
@@ -167,8 +177,6 @@ __global__ void __launch_bounds__(DGT, DGCTAS) distill_grad_kernel(const Distill
       if (mine) {
         float y = sc.gm * a.slot_g[(size_t)r * a.K + k];
         if (sc.glm != 0.f) y += (id == target ? sc.glm : 0.f) - sc.glm * expf(a.slot_lp[(size_t)r * a.K + k]);
-        // 0 times infinity at a token that is not legal
-        if (!(fabsf(y) < INFINITY) && !((!MASK || ((bm[id >> 5] >> (id & 31)) & 1u)) && TY::value(row[id]) > -INFINITY)) y = 0.f;
         list[slots + __popc(which & ((1u << lane) - 1))] = make_int2(id, __float_as_int(ldexpf(y / sc.Tm, sc.e)));
       }
       slots += __popc(which);

@@ -49,21 +49,25 @@ struct ProcessPlan {
   int bits;           // words of touched
 };
 
-// The row's numbers, and what becomes of a touched token.
+// The row's numbers, and what becomes of a touched token.  Penalties are finite, but their product
+// with a count (2^24 at most) may not be: those from 2^100 on are taken, like the logits, 2^26
+// times smaller, where only bits below 2^-124 are lost.
 struct ProcessRow {
-  float theta, presence, frequency;
+  float theta, presence, frequency, scale;
 };
+__device__ __forceinline__ ProcessRow process_row(const ProcessArgs& a, int r) {
+  ProcessRow p{a.repetition ? a.repetition[r] : 1.f, a.presence ? a.presence[r] : 0.f, a.frequency ? a.frequency[r] : 0.f, 1.f};
+  if (fmaxf(fabsf(p.presence), fabsf(p.frequency)) >= 0x1p100f) p.scale = 0x1p-26f;
+  p.presence *= p.scale;
+  p.frequency *= p.scale;
+  return p;
+}
 __device__ __forceinline__ float process_penalty(const ProcessRow& p, float v, uint32_t n) {
   if (n & (PSEEN | PCOUNT)) {
     v = v > 0.f ? __fdiv_rn(v, p.theta) : __fmul_rn(v, p.theta);
-    const float copies = (float)(n & PCOUNT);
-    const float presence = copies > 0.f ? p.presence : 0.f, take = __fadd_rn(__fmul_rn(p.frequency, copies), presence);
-    if (fabsf(take) < INFINITY) {
-      v = __fsub_rn(v, take);
-    } else {  // past binary32, of numbers that are not: the same steps, 2^26 times smaller
-      constexpr float c = 0x1p-26f;
-      v = __fmul_rn(__fsub_rn(v * c, __fadd_rn(__fmul_rn(p.frequency * c, copies), presence * c)), 1.f / c);
-    }
+    const float copies = (float)(n & PCOUNT), take = __fadd_rn(__fmul_rn(p.frequency, copies), copies > 0.f ? p.presence : 0.f);
+    v = __fsub_rn(__fmul_rn(v, p.scale), take);
+    if (p.scale != 1.f) v = __fmul_rn(v, 0x1p26f);
   }
   return v;
 }
@@ -132,8 +136,7 @@ __global__ void __launch_bounds__(PSPARSE, 2) process_sparse_kernel(const Proces
     id[k] = i < a.NB ? bias_ids[i] : -1;
     b[k] = i < a.NB ? bias[i] : 0.f;
   }
-  const ProcessRow p{a.repetition ? a.repetition[r] : 1.f, a.presence ? a.presence[r] : 0.f,
-                     a.frequency ? a.frequency[r] : 0.f};
+  const ProcessRow p = process_row(a, r);
   const int length = a.lengths ? a.lengths[r] : a.H, prompt = a.prompts ? a.prompts[r] : 0;
   bool bad = !process_valid(p, length, prompt, a.H);
 #pragma unroll
@@ -229,8 +232,7 @@ __global__ void __launch_bounds__(PT, PT == PSMALL ? PCTAS : PDENSECTAS) process
   const int32_t* history = a.history + (size_t)r * a.hld;
   const int32_t* bias_ids = a.bias_ids + (size_t)r * a.NB;
   const float* bias = a.bias + (size_t)r * a.NB;
-  const ProcessRow p{a.repetition ? a.repetition[r] : 1.f, a.presence ? a.presence[r] : 0.f,
-                     a.frequency ? a.frequency[r] : 0.f};
+  const ProcessRow p = process_row(a, r);
   const int length = a.lengths ? a.lengths[r] : a.H, prompt = a.prompts ? a.prompts[r] : 0;
   // the first of the history and the biases, on their way with the parameters
   int early[PEARLY], bias_id = -1;
