@@ -19,7 +19,7 @@
 // Two values share an instruction (add, fused multiply-add, multiply).  The slots are
 // written over a step's vectors by the same warp right after them, while their lines are
 // in L2, and are looked up by each warp for itself, so that no warp waits for another.
-// 4096 x 128256 bf16 with 64 slots: 316 us, 6.7 TB/s (a copy of as many bytes: 311); slots
+// 4096 x 128256 bf16 with 64 slots: 315 us, 6.7 TB/s (a copy of as many bytes: 311); slots
 // written at the end of each CTA 393, kept in a table of the CTA with two barriers 320,
 // logits through rings of bulk copies 341 to 351.
 #include "smp_train.cuh"

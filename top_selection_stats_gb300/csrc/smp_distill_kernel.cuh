@@ -13,7 +13,7 @@
 //
 // Bound by HBM where rows fill the SMs: 4096 x 128256 bf16 with 32 slots 157 us, 6.7 TB/s (a
 // copy of as many bytes: 156); 1024 x 256000 f16 with 128: 90 us (78), 2.25 rounds of rows.
-// One row of 128256: 7.5 us, a launch and the chain of slots, stream, cluster and finish.
+// One row of 128256: 7.6 us, a launch and the chain of slots, stream, cluster and finish.
 #pragma once
 
 #include "smp_distill.cuh"

@@ -200,6 +200,6 @@ def head_workspace(N, V, lib=None):
 
 
 def set_scoring_wait_limit(cycles=0, lib=None):
-    """smp_set_scoring_wait_limit: bound on each device wait of later token_logprobs and
-    head_logprobs calls of the process (SM cycles; 0 = default)."""
+    """smp_set_scoring_wait_limit: bound on each device wait of later token_logprobs,
+    head_logprobs and distill_loss calls of the process (SM cycles; 0 = default)."""
     _check((lib or load_library()).smp_set_scoring_wait_limit(int(cycles)), "smp_set_scoring_wait_limit")
