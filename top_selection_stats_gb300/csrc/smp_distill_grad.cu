@@ -58,7 +58,7 @@ struct DistillGradIn {
 __device__ __noinline__ DistillGradScale distill_grad_far(const DistillGradIn i) {
   DistillGradScale o;
   o.q.m = i.m;
-  if (!(fabsf(i.g) + fabsf(i.gl) < INFINITY)) {
+  if (!(fabsf(i.g) < INFINITY && fabsf(i.gl) < INFINITY)) {
     // An incoming gradient that is not finite: results that are not, at legal tokens alone.
     // Outside the slots 2^x is infinite for a finite logit and 0 for -inf, and D is 1, -1 or (NaN)
     // 0; a slot's value is 2^300 times what a sign comes to, 0 at a token without probability.

@@ -17,9 +17,10 @@
 //
 // Bound by HBM where rows are long and many: 1024 x 256000 f16 to binary32 248 us, 6.3 TB/s
 // (a copy of as many bytes: 233).  A result aligned unlike its logits, whose vectors are put
-// together from two, takes 1.4 to 1.7 times as long: 1000 x 128257 bf16 133 us, 88 alike.  Small calls are bound by the chain of a launch, parameters,
-// history, table and logits (1 x 128256 with 1000 entries 3.6 us), long histories by the
-// instructions that look through them in every CTA of the row.
+// together from two, takes 1.4 to 1.7 times as long: 1000 x 128257 bf16 133 us, 88 alike.
+// Small calls are bound by the chain of a launch, parameters, history, table and logits (1 x
+// 128256 with 1000 entries 3.6 us), long histories by the instructions that look through them
+// in every CTA of the row.
 #include "smp_score_kernel.cuh"
 #include "smp_train.cuh"
 
