@@ -10,7 +10,10 @@
 // D is handled as a mantissa and a power of two, so that neither a small T nor
 // gradients near the ends of binary32 make it 0 or infinite: usually 2^24 goes to
 // rho (2^x flushes results below 2^-126, which a small T would make visible), and the
-// whole power where it is beyond 2^60.
+// whole power where it is beyond 2^60.  In such rows the slots' values are taken at a scale
+// where the larger of g and g_lp is near 1, and D in binary64, where neither of its terms
+// hides the other; the rest of the kernel is the same for them, as anything more in it costs
+// all rows (values of the slots in binary64: 315 us to 348 or 356 for the case below).
 //
 // One read and one write of the row: bound by HBM.  A row is cut into segments, one per
 // CTA; a thread has DGU 16-byte vectors in flight and the next ones requested while it
@@ -82,10 +85,11 @@ __device__ __noinline__ DistillGradScale distill_grad_far(const DistillGradIn i)
   o.glm = ldexpf(i.gl, -ge);
   o.Tm = frexpf(i.T, &Te);
   o.e = ge - Te;
-  const float D = frexpf(o.gm * i.A - o.glm * i.mass, &De) / o.Tm;
-  De += o.e;
-  const int shift = De > -60 && De < 60 ? 24 : max(-250, min(250, De));
-  o.q.D = ldexpf(D, De - shift);
+  // in binary64, where neither product hides the other's bits
+  const double D = frexp(((double)i.g * i.A - (double)i.gl * i.mass) / i.T, &De);
+  // 2^(De - 1) at most goes to rho, so that rho 2^shift is in range where the result is
+  const int shift = D == 0.0 || (De > -60 && De <= 24) ? 24 : max(-250, min(250, De - 1));
+  o.q.D = (float)ldexp(D, De - shift);
   o.q.l2 = i.L / SC_LN2 - (float)shift;
   return o;
 }
@@ -101,7 +105,7 @@ __device__ __forceinline__ DistillGradScale distill_grad_scale(const DistillGrad
   o.q.l2 = i.L / SC_LN2 - 24.f;
   o.q.m = i.m;
   o.q.s = sc_scale(i.T);
-  if (!(i.T > 0x1p-30f && i.T < 0x1p20f && size > 0x1p-60f && size < 0x1p40f && fabsf(i.A) < 0x1p40f)) o = distill_grad_far(i);
+  if (!(i.T > 0x1p-20f && i.T < 0x1p20f && size > 0x1p-60f && size < 0x1p40f && fabsf(i.A) < 0x1p40f)) o = distill_grad_far(i);
   if (i.m == -INFINITY) o.q.m = o.q.l2 = o.q.D = 0.f;  // every legal token has a slot
   return o;
 }
@@ -239,6 +243,18 @@ __global__ void __launch_bounds__(DGT, DGCTAS) distill_grad_kernel(const Distill
       if (j == target) y += ldexpf(sc.glm / sc.Tm, sc.e);
       for (int k = 0; k < slots; ++k) y = list[k].x == j ? __int_as_float(list[k].y) : y;
       out[j] = TY::store(none ? 0.f : y);
+    }
+  }
+  // A target outside the slots whose two parts were infinite and opposite: (g A rho + gl (1 - p)) / T,
+  // by the warp that wrote it.
+  if (sc.e > 60 && target >= 0) {
+    const int v = (target + lead) / VE;
+    __syncwarp();
+    if (lane == 0 && (v < f0 || v >= f1 ? c == 0 && warp == 0 : v >= v0 && v < v1 && (v - v0) % DGT / 32 == warp) &&
+        isnan(TY::value(out[target])) && fabsf(a.g_lp[r]) < INFINITY && (!a.g_loss || fabsf(a.g_loss[r]) < INFINITY)) {
+      const float A = a.stats[4 * (size_t)r + 2], mass = a.stats[4 * (size_t)r + 3], p = expf(a.logprobs[r]);
+      const float rho = mass > 0.f ? __fdiv_rn(p, mass) : 0.f;
+      out[target] = TY::store(ldexpf((sc.gm * A * rho + sc.glm * (1.f - p)) / sc.Tm, sc.e));
     }
   }
 }
