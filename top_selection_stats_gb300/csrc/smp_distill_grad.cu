@@ -13,7 +13,7 @@
 // whole power where it is beyond 2^60.  In such rows the slots' values are taken at a scale
 // where the larger of g and g_lp is near 1, and D in binary64, where neither of its terms
 // hides the other; the rest of the kernel is the same for them, as anything more in it costs
-// all rows (values of the slots in binary64: 315 us to 348 or 356 for the case below).
+// all rows (values of the slots in binary64: 348 to 356 us for the case below).
 //
 // One read and one write of the row: bound by HBM.  A row is cut into segments, one per
 // CTA; a thread has DGU 16-byte vectors in flight and the next ones requested while it
@@ -22,7 +22,7 @@
 // Two values share an instruction (add, fused multiply-add, multiply).  The slots are
 // written over a step's vectors by the same warp right after them, while their lines are
 // in L2, and are looked up by each warp for itself, so that no warp waits for another.
-// 4096 x 128256 bf16 with 64 slots: 315 us, 6.7 TB/s (a copy of as many bytes: 311); slots
+// 4096 x 128256 bf16 with 64 slots: 316 us, 6.7 TB/s (a copy of as many bytes: 311); slots
 // written at the end of each CTA 393, kept in a table of the CTA with two barriers 320,
 // logits through rings of bulk copies 341 to 351.
 #include "smp_train.cuh"
